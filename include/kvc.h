@@ -359,6 +359,144 @@ kvc_status kvc_encode_pages_noalloc(const kvc_layout *layout, const kvc_codec *c
                                     void *out, size_t out_bytes, kvc_segment_desc *desc,
                                     void *stream);
 
+/* ------------------------------------------------------------------------
+ * Resident 8-bit cache.  The calls above move whole pages between an engine's
+ * 16-bit cache and an encoded buffer; these keep the cache itself in 8 bits
+ * on the GPU: tokens are quantised as they are written, attention reads the
+ * codes where they lie, and rows are read back into 16 bits (to be encoded
+ * for offload, or checked).  The scale rules are those of the codecs
+ * KVC_FP8_DYNAMIC and KVC_INT8, taken over a block -- the tokens of one page
+ * for one KV head -- instead of over one vector.
+ *
+ * A value is code * scale.  Codes are E4M3FN (never its NaN) or INT8 in
+ * [-127, 127]; every (page, head) has one FP32 scale for K and one for V:
+ *     k_codes  [page][head][token][D]       v_codes  [page][head][D][token]
+ *     k_scales [page][head]                 v_scales [page][head]
+ * V is token-minor: the attention kernel takes 16 consecutive positions of a
+ * dimension with one load, already in its matrix operand's order.
+ *
+ * These calls work on one layer, on the context's device.  They allocate
+ * nothing, copy nothing from the host, keep nothing between calls and may be
+ * captured into a graph.  What changes from step to step -- page ids, rows
+ * and lengths -- is read on the device, so a captured call follows it; the
+ * host checks everything it can see, the kernels check the rest against the
+ * bounds given here (an entry out of bounds is never followed) and report it
+ * in seq_flags.  kvc_validate_batch checks host copies of the arrays.  Calls
+ * that write a cache and calls that use it must be ordered by the caller (one
+ * stream, or events). */
+
+/* One layer's cache.  codec: KVC_FP8_DYNAMIC or KVC_INT8.  head_dim: 32, 64,
+ * 128 or 256; tokens_per_page: 16, 32, 64, 128 or 256 (else
+ * KVC_E_UNSUPPORTED).  stride_page: bytes between pages of k_codes and of
+ * v_codes, a multiple of 16, at least kv_heads * tokens_per_page * head_dim;
+ * stride_scale: floats between pages of k_scales and of v_scales, at least
+ * kv_heads.  Code pointers are 16-byte aligned, scale pointers 4-byte. */
+typedef struct {
+  uint32_t abi;                 /* KVC_ABI_VERSION */
+  uint32_t codec;
+  uint32_t kv_heads, head_dim, tokens_per_page;
+  uint32_t reserved;            /* 0 */
+  uint64_t num_pages;
+  int64_t stride_page, stride_scale;
+  void *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+} kvc_cache;
+
+/* The sequences of a call.  Position t of sequence b lies in page
+ * block_table[b * stride_table + t / tokens_per_page], at token t mod
+ * tokens_per_page.  Rows [cu_rows[b], cu_rows[b + 1]) of the call's row
+ * tensors are sequence b's last positions: with n of them, positions
+ * lengths[b] - n .. lengths[b] - 1 (rows that would come before position 0
+ * have none).  The three arrays are device memory; the bounds are the
+ * caller's promise for them:
+ *   n_rows    rows of the row tensors; cu_rows ends at or below it, and rows
+ *             behind the last sequence are left as they are;
+ *   max_rows  most rows of a sequence;
+ *   max_len   greatest length, at most stride_table * tokens_per_page.
+ * Launches are sized by the bounds, so tight ones are faster.
+ * seq_flags (device [n_seqs], may be NULL) collects KVC_SEQ_* bits; a call
+ * only ever sets bits, the caller clears them.  n_seqs and n_rows may be 0:
+ * nothing is enqueued.  n_seqs is at most 2^20, n_rows below 2^31. */
+typedef struct {
+  uint32_t n_seqs, n_rows, max_rows, max_len;
+  int64_t stride_table;
+  const int32_t *block_table, *cu_rows, *lengths;
+  uint32_t *seq_flags;
+} kvc_batch;
+enum {
+  KVC_SEQ_BAD_RANGE = 1,  /* rows or length outside the bounds: the sequence was skipped */
+  KVC_SEQ_BAD_PAGE = 2,   /* a page id outside [0, num_pages): its tokens were not written, read as
+                             zero, or hidden from attention */
+  KVC_SEQ_NONFINITE = 4   /* kvc_cache_write: a NaN was stored as 0, an infinity as the largest code */
+};
+
+/* A row tensor [n_rows][heads][head_dim] of dtype KVC_BF16 or KVC_FP16 with
+ * the innermost dimension contiguous, 16-byte aligned, strides (in elements)
+ * positive multiples of 8.  Rows that a call writes must not overlap. */
+typedef struct {
+  uint32_t dtype, heads;
+  int64_t stride_row, stride_head;
+  void *data;
+} kvc_rows;
+
+/* Write the rows k and v (kv_heads heads, one dtype) into their positions.
+ * For each page and head that receives tokens, a = the largest finite |x|
+ * among them and rule(a) = RN(max(a, 1e-12) * RN(1/448)) (E4M3FN) or
+ * RN(max(a, 1e-12) / 127) (INT8).  If the page's first token is among them
+ * the scale becomes rule(a): whatever the page held is gone.  Otherwise it
+ * becomes max(scale, rule(a)), and if it grew, the codes of the page's
+ * earlier tokens are quantised anew from RN(code * old scale).  Codes:
+ * RNE(RN(x / scale)), clipped to the type's range.  Bytes of positions
+ * outside the call's are left as they are, but for that.  A page must be
+ * written from its first token on before it is appended to, and must not be
+ * written by two sequences of a call (kvc_validate_batch reports that as
+ * KVC_E_DUP_DST; the codes are undefined then, but nothing else is). */
+kvc_status kvc_cache_write(kvc_ctx *ctx, const kvc_cache *cache, const kvc_batch *batch,
+                           const kvc_rows *k, const kvc_rows *v, void *stream);
+
+/* Read the rows' positions back into k and v: RN(RN(code * scale)), the outer
+ * rounding to their dtype.  Rows without a position are zero. */
+kvc_status kvc_cache_read(kvc_ctx *ctx, const kvc_cache *cache, const kvc_batch *batch,
+                          const kvc_rows *k, const kvc_rows *v, void *stream);
+
+/* Attention options.  q_heads: a multiple of kv_heads; query head x uses KV
+ * head x / (q_heads / kv_heads).  flags: KVC_ATTEND_CAUSAL, a row sees
+ * positions up to its own; without it, the whole length.  window: 0, or a row
+ * sees only positions after its own minus window.  scale: finite, positive. */
+#define KVC_ATTEND_CAUSAL 1u
+typedef struct {
+  uint32_t q_heads, flags, window;
+  float scale;
+} kvc_attend;
+
+/* Bytes of workspace that kvc_cache_attend needs for these bounds (0 when
+ * its context is not split).  Host only, like kvc_plan. */
+kvc_status kvc_plan_attend(const kvc_cache *cache, const kvc_batch *batch, const kvc_attend *options,
+                           size_t *workspace_bytes);
+
+/* out = softmax(scale * q K^T) V over the positions each row sees, for rows
+ * that are in the cache already (written by kvc_cache_write, usually with the
+ * same batch).  q and out: q_heads heads, one dtype.  lse (device float
+ * [n_rows][q_heads], may be NULL): the natural logarithm of each softmax's
+ * sum.  A row that sees nothing gets zeros and -infinity; a row of q with a
+ * NaN or an infinity gets NaN.  Scores, statistics and sums are FP32, the
+ * softmax weights enter the second product with 11 significant bits.  The V
+ * scales of the pages a row sees must lie within a factor of 2^120.
+ * workspace: device, 16-byte aligned, at least kvc_plan_attend's bytes; calls
+ * that may overlap (other streams, other graphs) need one each. */
+kvc_status kvc_cache_attend(kvc_ctx *ctx, const kvc_cache *cache, const kvc_batch *batch,
+                            const kvc_attend *options, const kvc_rows *q, const kvc_rows *out,
+                            float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Check host copies of a batch's arrays (block_table [n_seqs][stride_table],
+ * cu_rows [n_seqs + 1], lengths [n_seqs]) against its bounds and the cache:
+ * KVC_E_ARG for rows or lengths out of bounds, KVC_E_PAGE_RANGE for a page id
+ * outside [0, num_pages) below a sequence's length, KVC_E_DUP_DST when
+ * `writes` is not 0 and two sequences (or one, twice) would write a page.
+ * Host only. */
+kvc_status kvc_validate_batch(const kvc_cache *cache, const kvc_batch *batch, const int32_t *block_table,
+                              const int32_t *cu_rows, const int32_t *lengths, int writes);
+
 /* Short text for a status code (static storage). */
 const char *kvc_status_string(kvc_status s);
 

@@ -37,6 +37,9 @@ KVC_SEG_ENCODED, KVC_SEG_RAW_POLICY, KVC_SEG_RAW_DATA, KVC_SEG_CAPACITY, KVC_SEG
 KVC_FLAG_RAW_POLICY, KVC_FLAG_RAW_DATA, KVC_FLAG_CAPACITY, KVC_FLAG_CRC32, KVC_FLAG_HEAP = 1, 2, 4, 8, 16
 # kvc_codec.flags
 KVC_CODEC_CRC32 = 1
+# kvc_batch.seq_flags / kvc_attend.flags
+KVC_SEQ_BAD_RANGE, KVC_SEQ_BAD_PAGE, KVC_SEQ_NONFINITE = 1, 2, 4
+KVC_ATTEND_CAUSAL = 1
 # decode seg_status values
 DEC_OK, DEC_HEADER, DEC_GUARD, DEC_CRC = 0, 1, 2, 3
 
@@ -73,6 +76,30 @@ class kvc_segment_desc(ctypes.Structure):
                 ("crc32", ctypes.c_uint32)]
 
 
+class kvc_cache(ctypes.Structure):
+    _fields_ = [("abi", ctypes.c_uint32), ("codec", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("tokens_per_page", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("num_pages", ctypes.c_uint64), ("stride_page", ctypes.c_int64), ("stride_scale", ctypes.c_int64),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class kvc_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_uint32), ("n_rows", ctypes.c_uint32), ("max_rows", ctypes.c_uint32),
+                ("max_len", ctypes.c_uint32), ("stride_table", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("cu_rows", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("seq_flags", ctypes.c_void_p)]
+
+
+class kvc_rows(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("heads", ctypes.c_uint32), ("stride_row", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class kvc_attend(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("window", ctypes.c_uint32),
+                ("scale", ctypes.c_float)]
+
+
 DESC_DTYPE = np.dtype([("offset", "<u8"), ("spill_offset", "<u8"), ("stored_len", "<u4"),
                        ("original_len", "<u4"), ("version", "u1"), ("format", "u1"),
                        ("flags", "u1"), ("status", "u1"), ("crc32", "<u4")])
@@ -80,7 +107,8 @@ assert DESC_DTYPE.itemsize == ctypes.sizeof(kvc_segment_desc) == 32
 
 EXPORTS = ["kvc_create", "kvc_destroy", "kvc_plan", "kvc_validate_encode", "kvc_validate_decode",
            "kvc_encode_pages", "kvc_decode_pages", "kvc_decode_layers", "kvc_offload_pages",
-           "kvc_restore_pages", "kvc_encode_pages_noalloc", "kvc_status_string"]
+           "kvc_restore_pages", "kvc_encode_pages_noalloc", "kvc_status_string",
+           "kvc_cache_write", "kvc_cache_read", "kvc_plan_attend", "kvc_cache_attend", "kvc_validate_batch"]
 
 _lib = None
 
@@ -126,6 +154,15 @@ def lib():
         L.kvc_encode_pages_noalloc.restype = st
         L.kvc_encode_pages_noalloc.argtypes = [ctypes.POINTER(kvc_layout), ctypes.POINTER(kvc_codec), P,
                                                ctypes.c_uint32, P, ctypes.c_size_t, P, P]
+        for name in ("kvc_cache_write", "kvc_cache_read"):
+            getattr(L, name).restype = st
+            getattr(L, name).argtypes = [P, P, P, P, P, P]
+        L.kvc_plan_attend.restype = st
+        L.kvc_plan_attend.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_size_t)]
+        L.kvc_cache_attend.restype = st
+        L.kvc_cache_attend.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        L.kvc_validate_batch.restype = st
+        L.kvc_validate_batch.argtypes = [P, P, P, P, P, ctypes.c_int]
         L.kvc_status_string.restype = ctypes.c_char_p
         L.kvc_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -301,3 +338,168 @@ def kvc_restore_pages(ctx, layout: Layout, codec: Codec, host_ptr: int, host_byt
                                    ptr, arr.size, layer_begin, layer_end, seg_status_ptr or None,
                                    ctypes.cast(evs, ctypes.c_void_p) if evs is not None else None,
                                    stream or None), "kvc_restore_pages")
+
+
+# --------------------------------------------------------------- resident 8-bit cache
+class Cache:
+    """Owns a kvc_cache: one layer's codes and scales.
+
+    k_codes [pages, H, T, D], v_codes [pages, H, D, T] (torch.float8_e4m3fn or
+    torch.int8), k_scales, v_scales [pages, H] (float32); pages may be strided,
+    each one's codes are contiguous.  The tensors are kept alive.
+    """
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        import torch
+        codec = {torch.float8_e4m3fn: CODECS["FP8_DYNAMIC"], torch.int8: CODECS["INT8"]}.get(k_codes.dtype)
+        if codec is None or v_codes.dtype != k_codes.dtype:
+            raise ValueError(f"unsupported cache dtypes {k_codes.dtype}, {v_codes.dtype}")
+        pages, H, T, D = k_codes.shape
+        if tuple(v_codes.shape) != (pages, H, D, T):
+            raise ValueError(f"v_codes must be [pages, heads, head_dim, tokens]: {tuple(v_codes.shape)}")
+        for s in (k_scales, v_scales):
+            if s.dtype != torch.float32 or tuple(s.shape) != (pages, H):
+                raise ValueError("scales must be float32 [pages, heads]")
+        one = pages == 1
+        sp = H * T * D if one else k_codes.stride(0)
+        ss = H if one else k_scales.stride(0)
+        if k_codes[0].is_contiguous() is False or v_codes[0].is_contiguous() is False or \
+                k_scales[0].is_contiguous() is False or v_scales[0].is_contiguous() is False or \
+                (not one and (v_codes.stride(0) != sp or v_scales.stride(0) != ss)):
+            raise ValueError("pages must be contiguous, K's and V's at one stride")
+        self.tensors = (k_codes, v_codes, k_scales, v_scales)
+        self.c = kvc_cache(KVC_ABI_VERSION, codec, H, D, T, 0, pages, sp, ss, *(t.data_ptr() for t in self.tensors))
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def empty(num_pages, kv_heads, head_dim, tokens_per_page, codec="FP8_DYNAMIC", device="cuda"):
+        """A cache of unwritten pages (zeros)."""
+        import torch
+        dt = {"FP8_DYNAMIC": torch.float8_e4m3fn, "INT8": torch.int8}[codec]
+        k = torch.zeros((num_pages, kv_heads, tokens_per_page, head_dim), dtype=torch.int8, device=device).view(dt)
+        v = torch.zeros((num_pages, kv_heads, head_dim, tokens_per_page), dtype=torch.int8, device=device).view(dt)
+        ks, vs = (torch.zeros((num_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2))
+        return Cache(k, v, ks, vs)
+
+
+class Batch:
+    """Owns a kvc_batch: block_table [seqs, columns], cu_rows [seqs + 1],
+    lengths [seqs] (int32, on the GPU, kept alive) and their bounds.
+    seq_flags: int32 [seqs] or None."""
+
+    def __init__(self, block_table, cu_rows, lengths, n_rows, max_rows, max_len, seq_flags=None):
+        import torch
+        n = lengths.shape[0]
+        for t in (block_table, cu_rows, lengths) + ((seq_flags,) if seq_flags is not None else ()):
+            if t.dtype != torch.int32:
+                raise ValueError("block_table, cu_rows, lengths and seq_flags are int32")
+        if block_table.dim() != 2 or block_table.shape[0] != n or tuple(cu_rows.shape) != (n + 1,) or \
+                (seq_flags is not None and tuple(seq_flags.shape) != (n,)):
+            raise ValueError("block_table [seqs, columns], cu_rows [seqs + 1], lengths [seqs], seq_flags [seqs]")
+        if not all(t.is_contiguous() for t in (cu_rows, lengths)) or \
+                (seq_flags is not None and not seq_flags.is_contiguous()) or \
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("cu_rows, lengths, seq_flags and the rows of block_table are contiguous")
+        # a row of the table is read up to its own columns only, whatever its stride
+        columns = block_table.shape[1]
+        stride = block_table.stride(0) if n > 1 else columns
+        if stride < columns:
+            raise ValueError("rows of block_table overlap")
+        self.columns = columns
+        self.tensors = (block_table, cu_rows, lengths, seq_flags)
+        self.c = kvc_batch(n, n_rows, max_rows, max_len, stride, block_table.data_ptr() or None,
+                           cu_rows.data_ptr() or None, lengths.data_ptr() or None,
+                           seq_flags.data_ptr() if seq_flags is not None else None)
+        self.ref = ctypes.byref(self.c)
+
+
+class Rows:
+    """Owns a kvc_rows over a tensor [rows, heads, head_dim] (kept alive)."""
+
+    def __init__(self, t):
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+            raise ValueError("row tensors are [rows, heads, head_dim], contiguous along head_dim")
+        self.tensor = t
+        n, heads, d = t.shape
+        # strides of extents of 1 are never used: any valid ones will do
+        sh = t.stride(1) if heads > 1 else d
+        sr = t.stride(0) if n > 1 else heads * sh
+        self.c = kvc_rows(_dtype_code(t), heads, sr, sh, t.data_ptr() or None)
+        self.shape = (n, heads, d)
+        self.ref = ctypes.byref(self.c)
+
+
+class Attend:
+    """Owns a kvc_attend.  scale: None is 1 / sqrt(head_dim), set on use."""
+
+    def __init__(self, q_heads, causal=True, window=0, scale=None):
+        self.scale = scale
+        self.c = kvc_attend(q_heads, KVC_ATTEND_CAUSAL if causal else 0, window, scale or 0.0)
+        self.ref = ctypes.byref(self.c)
+
+    def of(self, cache):
+        if self.scale is None:
+            self.c.scale = cache.c.head_dim ** -0.5
+        return self.ref
+
+
+def _rows(t, cache, batch):
+    r = t if isinstance(t, Rows) else Rows(t)
+    if r.shape[0] < batch.c.n_rows or r.shape[2] != cache.c.head_dim:
+        raise ValueError(f"rows {r.shape}: need {batch.c.n_rows} rows of head_dim {cache.c.head_dim}")
+    return r
+
+
+def _table_ok(cache, batch):
+    if batch.c.max_len > batch.columns * cache.c.tokens_per_page:
+        raise KvcError(KVC_E_ARG, "Batch: max_len is beyond block_table's columns")
+
+
+def kvc_cache_write(ctx, cache: Cache, batch: Batch, k, v, stream: int = 0):
+    """k, v: tensors [rows, H, D] or Rows."""
+    _table_ok(cache, batch)
+    k, v = _rows(k, cache, batch), _rows(v, cache, batch)
+    _check(lib().kvc_cache_write(ctx, cache.ref, batch.ref, k.ref, v.ref, stream or None), "kvc_cache_write")
+
+
+def kvc_cache_read(ctx, cache: Cache, batch: Batch, k, v, stream: int = 0):
+    """k, v: tensors [rows, H, D] or Rows, written."""
+    _table_ok(cache, batch)
+    k, v = _rows(k, cache, batch), _rows(v, cache, batch)
+    _check(lib().kvc_cache_read(ctx, cache.ref, batch.ref, k.ref, v.ref, stream or None), "kvc_cache_read")
+
+
+def kvc_plan_attend(cache: Cache, batch: Batch, options: Attend) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kvc_plan_attend(cache.ref, batch.ref, options.of(cache), ctypes.byref(n)), "kvc_plan_attend")
+    return n.value
+
+
+def kvc_cache_attend(ctx, cache: Cache, batch: Batch, options: Attend, q, out, lse=None, workspace=None,
+                     stream: int = 0):
+    """q, out: tensors [rows, q_heads, D] or Rows; lse: float32 [rows, q_heads]
+    or None; workspace: a uint8 tensor of kvc_plan_attend's bytes, or None."""
+    _table_ok(cache, batch)
+    q, out = _rows(q, cache, batch), _rows(out, cache, batch)
+    if lse is not None and (str(lse.dtype) != "torch.float32" or not lse.is_contiguous() or
+                            lse.dim() != 2 or lse.shape[0] < batch.c.n_rows or lse.shape[1] != options.c.q_heads):
+        raise ValueError("lse is a contiguous float32 [rows, q_heads]")
+    _check(lib().kvc_cache_attend(ctx, cache.ref, batch.ref, options.of(cache), q.ref, out.ref,
+                                  lse.data_ptr() if lse is not None else None,
+                                  workspace.data_ptr() if workspace is not None else None,
+                                  workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                  stream or None), "kvc_cache_attend")
+
+
+def kvc_validate_batch(cache: Cache, batch: Batch, block_table, cu_rows, lengths, writes: bool) -> int:
+    """Host copies of the batch's arrays; block_table [seqs, columns]."""
+    a = np.ascontiguousarray(np.asarray(block_table, np.int32))
+    cu, ln = (np.ascontiguousarray(np.asarray(x, np.int32)) for x in (cu_rows, lengths))
+    n = batch.c.n_seqs
+    if a.shape != (n, batch.columns) or cu.shape != (n + 1,) or ln.shape != (n,):
+        raise ValueError("block_table [seqs, columns], cu_rows [seqs + 1], lengths [seqs]")
+    _table_ok(cache, batch)
+    b = kvc_batch.from_buffer_copy(batch.c)
+    b.stride_table = batch.columns
+    return lib().kvc_validate_batch(cache.ref, ctypes.byref(b), a.ctypes.data, cu.ctypes.data, ln.ctypes.data,
+                                    int(bool(writes)))

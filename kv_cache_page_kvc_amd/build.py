@@ -5,11 +5,14 @@
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkvc.so")
-SOURCES = [os.path.join(HERE, "csrc", "kvc_host.cpp"), os.path.join(HERE, "csrc", "kvc_kernels.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f)
+           for f in ("kvc_host.cpp", "kvc_kernels.hip", "kvc_cache_rows.hip", "kvc_attend.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -24,15 +27,24 @@ FLAGS = [
 
 
 def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-           "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("hipcc failed building libkvc.so")
+    """Compile the sources side by side, then link them."""
+    with tempfile.TemporaryDirectory() as work:
+        def run(cmd):
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            return subprocess.run(cmd, capture_output=True, text=True)
+
+        objects = [os.path.join(work, os.path.basename(f) + ".o") for f in SOURCES]
+        compile_flags = [f for f in FLAGS if f != "-shared"] + ["-I", os.path.join(ROOT, "include"),
+                                                                "-I", os.path.join(HERE, "csrc"), "-c"]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            done = list(pool.map(lambda fo: run([HIPCC, *compile_flags, "-o", fo[1], fo[0]]), zip(SOURCES, objects)))
+        tmp = LIB + ".tmp"
+        if all(r.returncode == 0 for r in done):
+            done.append(run([HIPCC, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objects]))
+        if any(r.returncode != 0 for r in done):
+            sys.stderr.write("".join(r.stdout + r.stderr for r in done))
+            raise RuntimeError("hipcc failed building libkvc.so")
     os.replace(tmp, LIB)
     return LIB
 

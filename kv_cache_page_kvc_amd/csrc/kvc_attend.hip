@@ -1,0 +1,403 @@
+// kvc_attend.hip -- gfx950 attention over the resident 8-bit cache.
+//
+// For a query row i and the positions j it sees, with the page scales ks, vs:
+//   t_ij = log2(e) * scale * ks[page(j)] * <q_i, kcode_j> + log2(vs[page(j)])
+//   w_ij = 2^(t_ij - m_i),  m_i the running maximum of t_ij minus 15
+//   out_i = sum_j w_ij vcode_j / sum_j w_ij / vs[page(j)].
+// Folding log2(vs) into the exponent makes w the weight of a *code*: V's codes
+// then enter the product as they are, and w <= 2^15 is a binary16 value
+// whatever the pages' scales are.  Both products run on the matrix cores in
+// binary16 with binary32 sums: E4M3FN and INT8 codes are binary16 values
+// exactly, a query row is scaled by a power of two to a largest |q| in
+// [2^14, 2^15), which keeps every BF16 or FP16 value above 2^-29 of that
+// exact, and the weights are rounded to 11 significant bits (off by 2^-11 of
+// themselves at most, and by 2^-40 of the largest where they are below 2^-29
+// of it).  The denominator, the maxima and the merged sums are binary32.
+//
+// Registers instead of LDS.  A wave takes 64 positions at a time as 4 groups
+// of 16 (a group lies in one page).  Scores are computed transposed, S^T =
+// K Q^T, with row 4g + j of product tile i standing for position 16g + 4i + j:
+// after 4 tiles lane group g (16 lanes, one query row each) holds the scores
+// of the 16 positions of group g, which is exactly the operand layout of the
+// second product, out^T = V^T W^T, when V is stored token-minor.  So scores,
+// weights and both operands stay in registers, a lane's loads are 16
+// consecutive bytes of K (dimensions) and V (positions), and the running
+// maximum needs two lane swaps a row.
+#include "kvc_cache_device.h"
+
+namespace kvc {
+namespace {
+
+constexpr int kTile = 64;             // positions a wave takes at a time
+constexpr int kWaves = 4;             // waves of a workgroup
+constexpr float kShift = 15.0f;       // weights are at most 2^15
+// Page scales below this count as this: an empty page's scale may be 0.  The
+// scale rule gives at least 1e-12 / 448.
+constexpr float kMinScale = 0x1p-64f;
+
+// 8 codes -> 8 binary16 values, exactly
+template <uint32_t CODEC>
+__device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
+  union { f16x8 v; f16x2 p[4]; } r;
+  if constexpr (CODEC == C_FP8) {
+    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, false);
+    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, true);
+    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, false);
+    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, true);
+  } else {
+    // byte b + 128 below the exponent of 1024: 1024 + b + 128, less 1152
+    const uint32_t w[2] = {lo ^ 0x80808080u, hi ^ 0x80808080u};
+    const f16x2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      r.p[2 * i] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04010400u)) - off;
+      r.p[2 * i + 1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, w[i], 0x04030402u)) - off;
+    }
+  }
+  return r.v;
+}
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// one row tile of a sequence and KV head
+struct Tile {
+  Seq s;
+  int rows, row0;        // rows of the sequence (token * group + head), first of the tile
+  int begin, end;        // positions that some row of the tile sees
+  int all_from, all_to;  // positions that every row of the tile sees
+};
+__device__ __forceinline__ bool make_tile(const AttendParams& p, uint32_t unit, int m, Tile& t) {
+  t.s = seq_of_unit(p.b, unit);
+  if (!t.s.ok) return false;
+  const int64_t rows = (int64_t)t.s.n * p.group, row0 = (int64_t)t.s.unit * m;
+  if (row0 >= rows) return false;
+  t.rows = (int)rows;
+  t.row0 = (int)row0;
+  const int first = t.row0 / (int)p.group, last = min(t.rows - 1, t.row0 + m - 1) / (int)p.group;
+  t.end = p.causal ? max(0, min(t.s.len, t.s.start + last + 1)) : t.s.len;
+  t.all_to = p.causal ? min(t.s.len, t.s.start + first + 1) : t.s.len;
+  t.begin = p.window ? max(0, t.s.start + first - (int)p.window + 1) : 0;
+  t.all_from = p.window ? t.s.start + last - (int)p.window + 1 : 0;
+  return true;
+}
+
+// D: head size; NT: tile of 16 * NT query rows, the same for the workgroup's
+// four waves, which take the context's tiles in turn and are joined in LDS.
+template <int D, int NT, uint32_t CODEC>
+__global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) {
+  constexpr int M = 16 * NT, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
+  __shared__ float s_acc[kWaves / 2][M][D + 4];
+  __shared__ float s_m[kWaves][M], s_l[kWaves][M];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
+  const int split = (int)(rest % p.splits);
+  Tile t;
+  if (!make_tile(p, rest / p.splits, M, t)) return;
+  const int T = 1 << p.c.tshift, G = (int)p.group;
+  const int lo = max(t.begin, split * (int)p.chunk) / kTile,
+            hi = (int)min((int64_t)t.end, (int64_t)(split + 1) * p.chunk);
+
+  // query rows, scaled by a power of two
+  f16x8 q[NT][KS];
+  float crow[NT], m[NT], l[NT];
+  int from[NT], to[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const int r = t.row0 + 16 * nt + c, i = r / G;
+    const bool in = r < t.rows;
+    from[nt] = p.window ? t.s.start + i - (int)p.window + 1 : 0;
+    to[nt] = in ? (p.causal ? min(t.s.len, t.s.start + i + 1) : t.s.len) : 0;
+    const uint16_t* qp = p.q.data + (int64_t)(t.s.r0 + i) * p.q.stride_row + (int64_t)(h * G + r % G) * p.q.stride_head;
+    float x[KS][8];
+    float am = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) {
+      const int d = D >= 64 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 8 * g;
+      const uint4 w = in ? ld_global16(qp + d) : make_uint4(0, 0, 0, 0);
+      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const f32x2 f = p.dtype == KVC_BF16 ? unpack2<KVC_BF16>(a[j]) : unpack2<KVC_FP16>(a[j]);
+        x[ks][2 * j] = f.x;
+        x[ks][2 * j + 1] = f.y;
+        odd = odd || !(fabsf(f.x) < __builtin_inff()) || !(fabsf(f.y) < __builtin_inff());
+        am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    am = max_across_groups(am);
+    const float bad = max_across_groups(odd ? 1.0f : 0.0f);
+    const int e = am > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(am) : 0;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) q[nt][ks][j] = (_Float16)(bad != 0.0f ? 0.0f : ldexpf(x[ks][j], e));
+    // a row with an infinity or a NaN has no finite softmax
+    crow[nt] = bad != 0.0f ? __builtin_nanf("") : ldexpf(p.scale_log2, -e);
+    m[nt] = -__builtin_inff();
+    l[nt] = 0.0f;
+  }
+  f32x4 o[NT][NV];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int n = 0; n < NV; n++) o[nt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int32_t* table = p.b.table + (int64_t)t.s.b * p.b.stride_table;
+  const int last_group = (t.s.len - 1) >> 4;
+  bool bad_page = false;
+  for (int tile = lo + wave; tile * kTile < hi; tile += kWaves) {
+    const int base = tile * kTile;
+    // pages of this lane's group (scores, V) and of the group of its K rows
+    int32_t pv = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
+    int32_t pk = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
+    const bool okv = pv >= 0 && (uint32_t)pv < p.c.num_pages, okk = pk >= 0 && (uint32_t)pk < p.c.num_pages;
+    bad_page = bad_page || !okv;
+    pv = okv ? pv : 0;
+    pk = okk ? pk : 0;
+    const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
+    const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
+    const uint8_t* kp = p.c.k_codes + pk * p.c.stride_page + (int64_t)h * T * D + (gk + (c & 3)) * D;
+    const uint8_t* vp = p.c.v_codes + pv * p.c.stride_page + (int64_t)h * T * D + c * T + gv;
+    const float ks = p.c.k_scales[pv * p.c.stride_scale + h];
+    const float vs = fmaxf(p.c.v_scales[pv * p.c.stride_scale + h], kMinScale);
+    const int valid = okv ? min(max(t.s.len - base - 16 * g, 0), 16) : 0;   // positions of the group that are written
+    const float lvs = __builtin_amdgcn_logf(vs), ivs = __builtin_amdgcn_rcpf(vs);
+
+    f32x4 sc[NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) sc[nt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (D >= 64) {
+#pragma unroll
+        for (int ch = 0; ch < CH; ch++) {
+          const uint4 w = ld_global16(kp + 4 * i * D + 64 * ch + 16 * g);
+          const f16x8 a0 = codes_f16<CODEC>(w.x, w.y), a1 = codes_f16<CODEC>(w.z, w.w);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            sc[nt][i] = mfma(a0, q[nt][2 * ch], sc[nt][i]);
+            sc[nt][i] = mfma(a1, q[nt][2 * ch + 1], sc[nt][i]);
+          }
+        }
+      } else {
+        const uint2 w = ld_global8(kp + 4 * i * D + 8 * g);
+        const f16x8 a0 = codes_f16<CODEC>(w.x, w.y);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) sc[nt][i] = mfma(a0, q[nt][0], sc[nt][i]);
+      }
+    }
+
+    const bool masked = base < t.all_from || base + kTile > t.all_to || __any(valid < 16);
+    f16x8 w[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const float kc = ks * crow[nt];
+      float x[4][4];
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          x[i][j] = fmaf(sc[nt][i][j], kc, lvs);
+          if (masked) {
+            const int off = 4 * i + j, pos = base + 16 * g + off;
+            x[i][j] = pos >= from[nt] && pos < to[nt] && off < valid ? x[i][j] : -__builtin_inff();
+          }
+          mx = fmaxf(mx, x[i][j]);
+        }
+      const float now = fmaxf(m[nt], max_across_groups(mx));
+      const float ref = now == -__builtin_inff() ? 0.0f : now - kShift;   // a row that has seen nothing yet
+      const float alpha = __builtin_amdgcn_exp2f(m[nt] - now);
+      const float keep = now == -__builtin_inff() ? 1.0f : alpha;
+      m[nt] = now;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const float e = __builtin_amdgcn_exp2f(x[i][j] - ref);
+          sum += e;
+          w[nt][i >> 1][4 * (i & 1) + j] = (_Float16)e;
+        }
+      l[nt] = fmaf(l[nt], keep, sum * ivs);
+#pragma unroll
+      for (int n = 0; n < NV; n++) o[nt][n] *= keep;
+    }
+
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      uint4 v = ld_global16(vp + (int64_t)16 * n * T);
+      if (masked) {
+        // codes of unwritten positions may be anything, NaN included
+        uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int k = valid - 4 * i;
+          a[i] = k >= 4 ? a[i] : (k <= 0 ? 0u : a[i] & ((1u << (8 * k)) - 1u));
+        }
+        v = make_uint4(a[0], a[1], a[2], a[3]);
+      }
+      const f16x8 a0 = codes_f16<CODEC>(v.x, v.y), a1 = codes_f16<CODEC>(v.z, v.w);
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        o[nt][n] = mfma(a0, w[nt][0], o[nt][n]);
+        o[nt][n] = mfma(a1, w[nt][1], o[nt][n]);
+      }
+    }
+  }
+  if (__any(bad_page)) flag_seq(p.b, t.s.b, KVC_SEQ_BAD_PAGE);
+
+  // join the waves: every wave brings its sums to the common maximum, then
+  // the upper half of the waves adds into the lower half, twice
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    l[nt] = sum_across_groups(l[nt]);
+    if (g == 0) {
+      s_m[wave][16 * nt + c] = m[nt];
+      s_l[wave][16 * nt + c] = l[nt];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int v = 0; v < kWaves; v++) top = fmaxf(top, s_m[v][16 * nt + c]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kWaves; v++) {
+      // a wave that saw nothing has sum 0 (and maximum -inf); a NaN sum stays one
+      const float lv = s_l[v][16 * nt + c];
+      sum += lv == 0.0f ? 0.0f : lv * __builtin_amdgcn_exp2f(s_m[v][16 * nt + c] - top);
+    }
+    const float f = l[nt] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[nt] - top);
+    m[nt] = top;
+    l[nt] = sum;
+#pragma unroll
+    for (int n = 0; n < NV; n++) o[nt][n] *= f;
+  }
+#pragma unroll
+  for (int half = kWaves / 2; half >= 1; half /= 2) {
+    if (wave >= half && wave < 2 * half)
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int n = 0; n < NV; n++)
+          *(f32x4*)&s_acc[wave - half][16 * nt + c][16 * n + 4 * g] = o[nt][n];
+    __syncthreads();
+    if (wave < half)
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int n = 0; n < NV; n++)
+          o[nt][n] += *(const f32x4*)&s_acc[wave][16 * nt + c][16 * n + 4 * g];
+    __syncthreads();
+  }
+  if (wave != 0) return;
+  const int64_t slots = (int64_t)p.b.n_rows * H * G;     // (row, query head) pairs of a split
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const int r = t.row0 + 16 * nt + c;
+    if (r >= t.rows) continue;
+    const int row = t.s.r0 + r / G, head = (int)h * G + r % G;
+    if (p.splits > 1) {
+      const int64_t at = split * slots + (int64_t)row * H * G + head;
+      float* acc = p.ws + at * D;
+#pragma unroll
+      for (int n = 0; n < NV; n++) *(f32x4*)(acc + 16 * n + 4 * g) = o[nt][n];
+      if (g == 0) {
+        float* ml = p.ws + p.splits * slots * D + at * 2;
+        ml[0] = m[nt];
+        ml[1] = l[nt];
+      }
+      continue;
+    }
+    const float inv = l[nt] == 0.0f ? 0.0f : 1.0f / l[nt];
+    uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
+#pragma unroll
+    for (int n = 0; n < NV; n++) {
+      const f32x4 y = o[nt][n] * inv;
+      const uint2 w = p.dtype == KVC_BF16 ? make_uint2(pack2<KVC_BF16>(y[0], y[1]), pack2<KVC_BF16>(y[2], y[3]))
+                                          : make_uint2(pack2<KVC_FP16>(y[0], y[1]), pack2<KVC_FP16>(y[2], y[3]));
+      st_global8(dst + 16 * n + 4 * g, w);
+    }
+    if (p.lse && g == 0)
+      p.lse[(int64_t)row * H * G + head] =
+          l[nt] == 0.0f ? -__builtin_inff() : (m[nt] - kShift + __builtin_amdgcn_logf(l[nt])) * 0.693147180559945309f;
+  }
+}
+
+// Joins the context splits of a row and query head: one wave each, the rows
+// of a tile in turn.
+template <int D, int M>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
+  constexpr int E = D >= 64 ? D / 64 : 1;                 // dimensions of a lane
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t H = p.c.heads, h = blockIdx.x % H;
+  const int G = (int)p.group;
+  Tile t;
+  if (!make_tile(p, blockIdx.x / H, M, t)) return;
+  const int64_t slots = (int64_t)p.b.n_rows * H * G;
+  for (int r = t.row0 + wave; r < min(t.rows, t.row0 + M); r += 4) {
+    const int row = t.s.r0 + r / G, head = (int)h * G + r % G;
+    const int64_t at0 = (int64_t)row * H * G + head;
+    const float* ml = p.ws + p.splits * slots * D;
+    float top = -__builtin_inff();
+    for (uint32_t s = 0; s < p.splits; s++) top = fmaxf(top, ml[(s * slots + at0) * 2]);
+    float l = 0.0f, y[E] = {};
+    for (uint32_t s = 0; s < p.splits; s++) {
+      const int64_t at = s * slots + at0;
+      const float m = ml[at * 2], sum = ml[at * 2 + 1];
+      if (sum == 0.0f) continue;
+      const float f = __builtin_amdgcn_exp2f(m - top);
+      l = fmaf(sum, f, l);
+      if (lane < D / E)
+#pragma unroll
+        for (int e = 0; e < E; e++) y[e] = fmaf(p.ws[at * D + lane * E + e], f, y[e]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
+    if (lane < D / E)
+#pragma unroll
+      for (int e = 0; e < E; e++)
+        dst[lane * E + e] = (uint16_t)(p.dtype == KVC_BF16 ? pack2<KVC_BF16>(y[e] * inv, 0.0f)
+                                                           : pack2<KVC_FP16>(y[e] * inv, 0.0f));
+    if (p.lse && lane == 0)
+      p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+  }
+}
+
+template <int D, int NT>
+hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t stream) {
+  const dim3 grid(p.units * p.splits * p.c.heads);
+  if (codec == C_FP8) attend_kernel<D, NT, C_FP8><<<grid, 64 * kWaves, 0, stream>>>(p);
+  else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.splits > 1) {
+    attend_join_kernel<D, 16 * NT><<<p.units * p.c.heads, 256, 0, stream>>>(p);
+    e = hipGetLastError();
+  }
+  return e;
+}
+template <int D>
+hipError_t launch_tile(const AttendParams& p, uint32_t codec, uint32_t rows, hipStream_t stream) {
+  return rows == 16 ? launch_codec<D, 1>(p, codec, stream) : launch_codec<D, 2>(p, codec, stream);
+}
+
+}  // namespace
+
+hipError_t launch_cache_attend(const AttendParams& p, uint32_t codec, uint32_t head_dim, uint32_t tile_rows,
+                               hipStream_t stream) {
+  switch (head_dim) {
+    case 32: return launch_tile<32>(p, codec, tile_rows, stream);
+    case 64: return launch_tile<64>(p, codec, tile_rows, stream);
+    case 128: return launch_tile<128>(p, codec, tile_rows, stream);
+    case 256: return launch_tile<256>(p, codec, tile_rows, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace kvc

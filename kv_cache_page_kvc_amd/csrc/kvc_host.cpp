@@ -28,6 +28,7 @@
 #include <vector>
 
 #include "kvc.h"
+#include "kvc_cache.h"
 #include "kvc_internal.h"
 
 using namespace kvc;
@@ -661,6 +662,168 @@ hipError_t run_decode(const CallParams& P, const kvc_layout* L, const Plan& plan
   return e;
 }
 
+// ------------------------------------------------------------------ resident 8-bit cache
+// every index the kernels form from these fits 32 bits
+constexpr uint64_t kMaxSeqs = 1u << 20, kMaxRows = 1u << 30, kMaxLen = 1u << 30;
+
+kvc_status check_cache(const kvc_cache* c) {
+  if (!c || c->abi != KVC_ABI_VERSION || c->reserved) return KVC_E_ARG;
+  if (c->codec != KVC_FP8_DYNAMIC && c->codec != KVC_INT8) return KVC_E_UNSUPPORTED;
+  const uint32_t D = c->head_dim, T = c->tokens_per_page;
+  if (D != 32 && D != 64 && D != 128 && D != 256) return KVC_E_UNSUPPORTED;
+  if (T != 16 && T != 32 && T != 64 && T != 128 && T != 256) return KVC_E_UNSUPPORTED;
+  if (c->kv_heads == 0 || c->kv_heads > 65535) return KVC_E_ARG;
+  if (c->num_pages == 0 || c->num_pages > (uint64_t)std::numeric_limits<int32_t>::max()) return KVC_E_ARG;
+  if (c->stride_page < (int64_t)c->kv_heads * T * D || c->stride_page % 16) return KVC_E_ARG;
+  if (c->stride_scale < (int64_t)c->kv_heads) return KVC_E_ARG;
+  // the pools' extents stay within 63 bits
+  if (c->stride_page > std::numeric_limits<int64_t>::max() / (int64_t)c->num_pages ||
+      c->stride_scale > std::numeric_limits<int64_t>::max() / 4 / (int64_t)c->num_pages)
+    return KVC_E_ARG;
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return KVC_E_ARG;
+  if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & 15) return KVC_E_ARG;
+  if (((uintptr_t)c->k_scales | (uintptr_t)c->v_scales) & 3) return KVC_E_ARG;
+  return KVC_OK;
+}
+
+// the bounds of a batch (arrays = true: its device pointers as well)
+kvc_status check_batch(const kvc_cache* c, const kvc_batch* b, bool arrays) {
+  if (!b || b->n_seqs > kMaxSeqs || b->n_rows > kMaxRows || b->max_len > kMaxLen || b->stride_table < 0)
+    return KVC_E_ARG;
+  // (max_len + T - 1) / T page ids are read of a block table row
+  if ((b->max_len + (uint64_t)c->tokens_per_page - 1) / c->tokens_per_page > (uint64_t)b->stride_table)
+    return KVC_E_ARG;
+  if (b->stride_table > (int64_t)kMaxLen) return KVC_E_ARG;
+  if (arrays && b->n_seqs && b->n_rows) {
+    if (!b->cu_rows || !b->lengths || (!b->block_table && b->max_len)) return KVC_E_ARG;
+    if (((uintptr_t)b->cu_rows | (uintptr_t)b->lengths | (uintptr_t)b->block_table | (uintptr_t)b->seq_flags) & 3)
+      return KVC_E_ARG;
+  }
+  return KVC_OK;
+}
+
+kvc_status check_rows(const kvc_rows* r, uint32_t heads, uint32_t d, uint32_t n_rows, bool output) {
+  if (!r) return KVC_E_ARG;
+  if (r->dtype != KVC_BF16 && r->dtype != KVC_FP16) return KVC_E_UNSUPPORTED;
+  if (r->heads != heads) return KVC_E_ARG;
+  const int64_t sr = r->stride_row, sh = r->stride_head;
+  if (sr <= 0 || sh <= 0 || (sr % 8) || (sh % 8)) return KVC_E_ARG;
+  const int64_t most = std::numeric_limits<int64_t>::max() / 8;
+  if (sr > most / (int64_t)std::max(n_rows, 1u) || sh > most / (int64_t)heads) return KVC_E_ARG;
+  if (output) {
+    const bool by_row = sh >= (int64_t)d && sr >= (int64_t)(heads - 1) * sh + (int64_t)d;
+    const bool by_head = sr >= (int64_t)d && sh >= ((int64_t)n_rows - 1) * sr + (int64_t)d;
+    if (!by_row && !by_head) return KVC_E_ARG;
+  }
+  if (n_rows && (!r->data || ((uintptr_t)r->data & 15))) return KVC_E_ARG;
+  return KVC_OK;
+}
+
+kvc_status check_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o) {
+  if (!o || (o->flags & ~KVC_ATTEND_CAUSAL)) return KVC_E_ARG;
+  if (o->q_heads == 0 || o->q_heads % c->kv_heads || o->q_heads > kMaxSeqs) return KVC_E_ARG;
+  if (!(o->scale > 0.0f) || !(o->scale <= std::numeric_limits<float>::max())) return KVC_E_ARG;
+  // rows of a sequence and KV head, as the kernels count them
+  if ((uint64_t)std::min(b->max_rows, b->n_rows) * (o->q_heads / c->kv_heads) > kMaxRows) return KVC_E_ARG;
+  return KVC_OK;
+}
+
+CacheView cache_view(const kvc_cache* c) {
+  CacheView v{};
+  v.k_codes = static_cast<uint8_t*>(c->k_codes);
+  v.v_codes = static_cast<uint8_t*>(c->v_codes);
+  v.k_scales = c->k_scales;
+  v.v_scales = c->v_scales;
+  v.stride_page = c->stride_page;
+  v.stride_scale = c->stride_scale;
+  v.num_pages = (uint32_t)c->num_pages;
+  v.heads = c->kv_heads;
+  while ((1u << v.tshift) < c->tokens_per_page) v.tshift++;
+  return v;
+}
+
+// The batch, cut into units of `div` / `mul` rows with `add` more for each
+// sequence: one number for every sequence where that takes no more units
+// than the rows' own places do (seq_of_unit), which needs no search.
+BatchView batch_view(const kvc_batch* b, uint64_t per_seq, uint32_t mul, uint32_t div, uint32_t add, uint64_t* units) {
+  BatchView v{};
+  v.table = b->block_table;
+  v.cu = b->cu_rows;
+  v.lengths = b->lengths;
+  v.flags = b->seq_flags;
+  v.stride_table = b->stride_table;
+  v.n_seqs = b->n_seqs;
+  v.n_rows = b->n_rows;
+  v.max_rows = std::min(b->max_rows, b->n_rows);
+  v.max_len = b->max_len;
+  v.unit_mul = mul;
+  v.unit_div = div;
+  v.unit_add = add;
+  const uint64_t direct = per_seq * b->n_seqs, placed = (uint64_t)b->n_rows * mul / div + (uint64_t)b->n_seqs * add;
+  v.per_seq = direct <= placed ? (uint32_t)per_seq : 0;
+  *units = direct <= placed ? direct : placed;
+  return v;
+}
+
+RowsView rows_view(const kvc_rows* r) {
+  return RowsView{static_cast<uint16_t*>(r->data), r->stride_row, r->stride_head};
+}
+
+// write and read: a unit is a page of a sequence; n rows from any position on
+// touch at most (n + T - 2) / T + 1 pages
+kvc_status rows_call(kvc_ctx* ctx, const kvc_cache* c, const kvc_batch* b, const kvc_rows* k, const kvc_rows* v,
+                     bool write, void* stream) {
+  kvc_status st = check_cache(c);
+  if (st == KVC_OK) st = check_batch(c, b, true);
+  if (st == KVC_OK) st = check_rows(k, c->kv_heads, c->head_dim, b->n_rows, !write);
+  if (st == KVC_OK) st = check_rows(v, c->kv_heads, c->head_dim, b->n_rows, !write);
+  if (st != KVC_OK) return st;
+  if (k->dtype != v->dtype || !ctx) return KVC_E_ARG;
+  if (b->n_seqs == 0 || b->n_rows == 0) return KVC_OK;
+  const uint64_t T = c->tokens_per_page, most = std::min(b->max_rows, b->n_rows);
+  RowsParams P{};
+  uint64_t units = 0;
+  P.c = cache_view(c);
+  P.b = batch_view(b, most ? (most + T - 2) / T + 1 : 1, 1, (uint32_t)T, 2, &units);
+  P.k = rows_view(k);
+  P.v = rows_view(v);
+  P.units = (uint32_t)units;
+  if (units * c->kv_heads * 2 / 4 >= 0x7FFFFFFFull) return KVC_E_ARG;
+  if (!(write ? launch_cache_write : launch_cache_read)) return KVC_E_HIP;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return KVC_E_HIP;
+  const hipError_t e = (write ? launch_cache_write : launch_cache_read)(P, c->codec, k->dtype, c->head_dim,
+                                                                        static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? KVC_OK : KVC_E_HIP;
+}
+
+// How an attend call is cut: row tiles of `rows` query rows (tokens x heads
+// of a group), and context splits of `chunk` positions where the tiles alone
+// do not fill the device.
+struct AttendPlan {
+  BatchView b;
+  uint64_t units = 0;
+  uint32_t rows = 16, splits = 1, chunk = 0;
+  size_t workspace = 0;
+};
+constexpr uint64_t kAttendGroups = 1024;     // workgroups that fill 256 CUs
+constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
+kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
+  const uint32_t G = o->q_heads / c->kv_heads;
+  const uint64_t most = (uint64_t)std::min(b->max_rows, b->n_rows) * G;
+  p->rows = most <= 16 ? 16 : 32;
+  p->b = batch_view(b, std::max<uint64_t>(1, (most + p->rows - 1) / p->rows), G, p->rows, 1, &p->units);
+  const uint64_t groups = p->units * c->kv_heads;
+  uint64_t splits = groups ? (kAttendGroups + groups - 1) / groups : 1;
+  splits = std::min<uint64_t>(splits, (b->max_len + kAttendChunk - 1) / kAttendChunk);
+  splits = std::max<uint64_t>(splits, 1);
+  p->chunk = (uint32_t)align_up((b->max_len + splits - 1) / splits, kAttendChunk);
+  p->splits = std::max<uint32_t>(1, p->chunk ? (uint32_t)((b->max_len + p->chunk - 1) / p->chunk) : 1);
+  if (groups * p->splits > 0x7FFFFFFFull) return KVC_E_ARG;
+  p->workspace = p->splits == 1 ? 0 : (size_t)p->splits * b->n_rows * o->q_heads * (c->head_dim + 2) * sizeof(float);
+  return KVC_OK;
+}
+
 // Host containers can throw std::bad_alloc; no exception crosses the C ABI.
 template <class F>
 kvc_status no_throw(F&& f) noexcept {
@@ -1069,6 +1232,96 @@ kvc_status kvc_encode_pages_noalloc(const kvc_layout* layout, const kvc_codec* c
     P.seg_status = nullptr;
     const uint64_t nseg = (uint64_t)layout->layers * n_pages * 2;
     return run_encode(P, layout, plan, nseg, s) == hipSuccess ? KVC_OK : KVC_E_HIP;
+  });
+}
+
+kvc_status kvc_cache_write(kvc_ctx* ctx, const kvc_cache* cache, const kvc_batch* batch, const kvc_rows* k,
+                           const kvc_rows* v, void* stream) {
+  return no_throw([&]() -> kvc_status { return rows_call(ctx, cache, batch, k, v, true, stream); });
+}
+
+kvc_status kvc_cache_read(kvc_ctx* ctx, const kvc_cache* cache, const kvc_batch* batch, const kvc_rows* k,
+                          const kvc_rows* v, void* stream) {
+  return no_throw([&]() -> kvc_status { return rows_call(ctx, cache, batch, k, v, false, stream); });
+}
+
+kvc_status kvc_plan_attend(const kvc_cache* cache, const kvc_batch* batch, const kvc_attend* options,
+                           size_t* workspace_bytes) {
+  return no_throw([&]() -> kvc_status {
+    kvc_status st = check_cache(cache);
+    if (st == KVC_OK) st = check_batch(cache, batch, false);
+    if (st == KVC_OK) st = check_attend(cache, batch, options);
+    AttendPlan plan;
+    if (st == KVC_OK) st = plan_attend(cache, batch, options, &plan);
+    if (st == KVC_OK && workspace_bytes) *workspace_bytes = plan.workspace;
+    return st;
+  });
+}
+
+kvc_status kvc_cache_attend(kvc_ctx* ctx, const kvc_cache* cache, const kvc_batch* batch, const kvc_attend* options,
+                            const kvc_rows* q, const kvc_rows* out, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  return no_throw([&]() -> kvc_status {
+    kvc_status st = check_cache(cache);
+    if (st == KVC_OK) st = check_batch(cache, batch, true);
+    if (st == KVC_OK) st = check_attend(cache, batch, options);
+    if (st == KVC_OK) st = check_rows(q, options->q_heads, cache->head_dim, batch->n_rows, false);
+    if (st == KVC_OK) st = check_rows(out, options->q_heads, cache->head_dim, batch->n_rows, true);
+    if (st != KVC_OK) return st;
+    if (q->dtype != out->dtype || ((uintptr_t)lse & 3) || !ctx) return KVC_E_ARG;
+    AttendPlan plan;
+    st = plan_attend(cache, batch, options, &plan);
+    if (st != KVC_OK) return st;
+    if (batch->n_seqs == 0 || batch->n_rows == 0) return KVC_OK;
+    if (plan.workspace > workspace_bytes) return KVC_E_CAPACITY;
+    if (plan.workspace && (!workspace || ((uintptr_t)workspace & 15))) return KVC_E_ARG;
+    if (!launch_cache_attend) return KVC_E_HIP;
+    AttendParams P{};
+    P.c = cache_view(cache);
+    P.b = plan.b;
+    P.q = rows_view(q);
+    P.out = rows_view(out);
+    P.lse = lse;
+    P.ws = static_cast<float*>(workspace);
+    P.dtype = q->dtype;
+    P.group = options->q_heads / cache->kv_heads;
+    P.causal = options->flags & KVC_ATTEND_CAUSAL;
+    P.window = options->window < batch->max_len ? options->window : 0;   // a longer one hides nothing
+    P.scale_log2 = options->scale * 1.44269504088896340736f;
+    P.units = (uint32_t)plan.units;
+    P.splits = plan.splits;
+    P.chunk = plan.chunk;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return KVC_E_HIP;
+    const hipError_t e =
+        launch_cache_attend(P, cache->codec, cache->head_dim, plan.rows, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? KVC_OK : KVC_E_HIP;
+  });
+}
+
+kvc_status kvc_validate_batch(const kvc_cache* cache, const kvc_batch* batch, const int32_t* block_table,
+                              const int32_t* cu_rows, const int32_t* lengths, int writes) {
+  return no_throw([&]() -> kvc_status {
+    kvc_status st = check_cache(cache);
+    if (st == KVC_OK) st = check_batch(cache, batch, false);
+    if (st != KVC_OK) return st;
+    if (batch->n_seqs == 0) return KVC_OK;
+    if (!cu_rows || !lengths || (!block_table && batch->max_len)) return KVC_E_ARG;
+    const int64_t T = cache->tokens_per_page;
+    std::vector<int32_t> written;
+    for (uint32_t b = 0; b < batch->n_seqs; b++) {
+      const int64_t n = (int64_t)cu_rows[b + 1] - cu_rows[b], len = lengths[b];
+      if (cu_rows[b] < 0 || n < 0 || cu_rows[b + 1] > (int64_t)batch->n_rows || n > (int64_t)batch->max_rows ||
+          len < 0 || len > (int64_t)batch->max_len)
+        return KVC_E_ARG;
+      const int32_t* row = block_table + (int64_t)b * batch->stride_table;
+      for (int64_t i = 0; i * T < len; i++) {
+        if (row[i] < 0 || (uint64_t)row[i] >= cache->num_pages) return KVC_E_PAGE_RANGE;
+        if (writes && n > 0 && (i + 1) * T > len - n) written.push_back(row[i]);
+      }
+    }
+    std::sort(written.begin(), written.end());
+    return std::adjacent_find(written.begin(), written.end()) == written.end() ? KVC_OK : KVC_E_DUP_DST;
   });
 }
 
