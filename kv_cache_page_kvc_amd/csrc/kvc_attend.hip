@@ -65,20 +65,21 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
 struct Tile {
   Seq s;
   int rows, row0;        // rows of the sequence (token * group + head), first of the tile
-  int begin, end;        // positions that some row of the tile sees
+  int begin, end;        // positions that some row of the tile sees; begin is a multiple of kTile
   int all_from, all_to;  // positions that every row of the tile sees
 };
-__device__ __forceinline__ bool make_tile(const AttendParams& p, uint32_t unit, int m, Tile& t) {
-  t.s = seq_of_unit(p.b, unit);
+// the tile of m rows that starts at row0
+__device__ __forceinline__ bool make_tile(const AttendParams& p, const Seq& s, int64_t row0, int m, Tile& t) {
+  t.s = s;
   if (!t.s.ok) return false;
-  const int64_t rows = (int64_t)t.s.n * p.group, row0 = (int64_t)t.s.unit * m;
+  const int64_t rows = (int64_t)t.s.n * p.group;
   if (row0 >= rows) return false;
   t.rows = (int)rows;
   t.row0 = (int)row0;
   const int first = t.row0 / (int)p.group, last = min(t.rows - 1, t.row0 + m - 1) / (int)p.group;
   t.end = p.causal ? max(0, min(t.s.len, t.s.start + last + 1)) : t.s.len;
   t.all_to = p.causal ? min(t.s.len, t.s.start + first + 1) : t.s.len;
-  t.begin = p.window ? max(0, t.s.start + first - (int)p.window + 1) : 0;
+  t.begin = (p.window ? max(0, t.s.start + first - (int)p.window + 1) : 0) / kTile * kTile;
   t.all_from = p.window ? t.s.start + last - (int)p.window + 1 : 0;
   return true;
 }
@@ -88,16 +89,20 @@ __device__ __forceinline__ bool make_tile(const AttendParams& p, uint32_t unit, 
 template <int D, int NT, uint32_t CODEC>
 __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) {
   constexpr int M = 16 * NT, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
+  constexpr bool HOIST = D * NT <= 128;     // a tile's V loads go out with its K loads: room for both in registers
   __shared__ float s_acc[kWaves / 2][M][D + 4];
   __shared__ float s_m[kWaves][M], s_l[kWaves][M];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
   const int split = (int)(rest % p.splits);
   Tile t;
-  if (!make_tile(p, rest / p.splits, M, t)) return;
+  const Seq seq = seq_of_unit(p.b, rest / p.splits);
+  if (!make_tile(p, seq, (int64_t)seq.unit * M, M, t)) return;
   const int T = 1 << p.c.tshift, G = (int)p.group;
-  const int lo = max(t.begin, split * (int)p.chunk) / kTile,
-            hi = (int)min((int64_t)t.end, (int64_t)(split + 1) * p.chunk);
+  // this split's positions; the first one also stands for a tile that sees nothing
+  const int64_t from0 = t.begin + (int64_t)split * p.chunk;
+  if (split && from0 >= t.end) return;
+  const int lo = (int)(from0 / kTile), hi = (int)min((int64_t)t.end, from0 + p.chunk);
 
   // query rows, scaled by a power of two
   f16x8 q[NT][KS];
@@ -148,11 +153,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
   const int32_t* table = p.b.table + (int64_t)t.s.b * p.b.stride_table;
   const int last_group = (t.s.len - 1) >> 4;
   bool bad_page = false;
+  // page ids of a tile: of this lane's group (scores, V) and of the group of its K rows
+  auto page_ids = [&](int tile, int32_t& v, int32_t& k) {
+    v = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
+    k = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
+  };
+  int32_t next_v = 0, next_k = 0;
+  if ((lo + wave) * kTile < hi) page_ids(lo + wave, next_v, next_k);
   for (int tile = lo + wave; tile * kTile < hi; tile += kWaves) {
     const int base = tile * kTile;
-    // pages of this lane's group (scores, V) and of the group of its K rows
-    int32_t pv = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
-    int32_t pk = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
+    int32_t pv = next_v, pk = next_k;
+    page_ids(tile + kWaves, next_v, next_k);                // used one tile later
     const bool okv = pv >= 0 && (uint32_t)pv < p.c.num_pages, okk = pk >= 0 && (uint32_t)pk < p.c.num_pages;
     bad_page = bad_page || !okv;
     pv = okv ? pv : 0;
@@ -161,8 +172,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
     const uint8_t* kp = p.c.k_codes + pk * p.c.stride_page + (int64_t)h * T * D + (gk + (c & 3)) * D;
     const uint8_t* vp = p.c.v_codes + pv * p.c.stride_page + (int64_t)h * T * D + c * T + gv;
+    uint4 kr[4][CH], vr[NV];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int ch = 0; ch < CH; ch++) {
+        if constexpr (D >= 64) {
+          kr[i][ch] = ld_global16(kp + 4 * i * D + 64 * ch + 16 * g);
+        } else {
+          const uint2 w = ld_global8(kp + 4 * i * D + 8 * g);
+          kr[i][ch] = make_uint4(w.x, w.y, 0, 0);
+        }
+      }
     const float ks = p.c.k_scales[pv * p.c.stride_scale + h];
     const float vs = fmaxf(p.c.v_scales[pv * p.c.stride_scale + h], kMinScale);
+    if constexpr (HOIST)
+#pragma unroll
+      for (int n = 0; n < NV; n++) vr[n] = ld_global16(vp + (int64_t)16 * n * T);
     const int valid = okv ? min(max(t.s.len - base - 16 * g, 0), 16) : 0;   // positions of the group that are written
     const float lvs = __builtin_amdgcn_logf(vs), ivs = __builtin_amdgcn_rcpf(vs);
 
@@ -171,22 +197,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     for (int i = 0; i < 4; i++) {
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) sc[nt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (D >= 64) {
 #pragma unroll
-        for (int ch = 0; ch < CH; ch++) {
-          const uint4 w = ld_global16(kp + 4 * i * D + 64 * ch + 16 * g);
-          const f16x8 a0 = codes_f16<CODEC>(w.x, w.y), a1 = codes_f16<CODEC>(w.z, w.w);
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            sc[nt][i] = mfma(a0, q[nt][2 * ch], sc[nt][i]);
-            sc[nt][i] = mfma(a1, q[nt][2 * ch + 1], sc[nt][i]);
-          }
-        }
-      } else {
-        const uint2 w = ld_global8(kp + 4 * i * D + 8 * g);
+      for (int ch = 0; ch < CH; ch++) {
+        const uint4 w = kr[i][ch];
         const f16x8 a0 = codes_f16<CODEC>(w.x, w.y);
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) sc[nt][i] = mfma(a0, q[nt][0], sc[nt][i]);
+        for (int nt = 0; nt < NT; nt++) sc[nt][i] = mfma(a0, q[nt][2 * ch], sc[nt][i]);
+        if constexpr (D >= 64) {
+          const f16x8 a1 = codes_f16<CODEC>(w.z, w.w);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) sc[nt][i] = mfma(a1, q[nt][2 * ch + 1], sc[nt][i]);
+        }
       }
     }
 
@@ -194,31 +215,31 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     f16x8 w[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-      const float kc = ks * crow[nt];
-      float x[4][4];
-      float mx = -__builtin_inff();
+      const float kc = ks * crow[nt];                       // not negative
+      if (masked)
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          x[i][j] = fmaf(sc[nt][i][j], kc, lvs);
-          if (masked) {
+          for (int j = 0; j < 4; j++) {
             const int off = 4 * i + j, pos = base + 16 * g + off;
-            x[i][j] = pos >= from[nt] && pos < to[nt] && off < valid ? x[i][j] : -__builtin_inff();
+            sc[nt][i][j] = pos >= from[nt] && pos < to[nt] && off < valid ? sc[nt][i][j] : -__builtin_inff();
           }
-          mx = fmaxf(mx, x[i][j]);
-        }
+      float mx = sc[nt][0][0];
+#pragma unroll
+      for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[nt][e >> 2][e & 3]);
+      mx = mx == -__builtin_inff() ? mx : fmaf(mx, kc, lvs);   // kc may be 0
       const float now = fmaxf(m[nt], max_across_groups(mx));
       const float ref = now == -__builtin_inff() ? 0.0f : now - kShift;   // a row that has seen nothing yet
-      const float alpha = __builtin_amdgcn_exp2f(m[nt] - now);
-      const float keep = now == -__builtin_inff() ? 1.0f : alpha;
+      const float keep = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
       m[nt] = now;
+      const float shift = lvs - ref;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const float e = __builtin_amdgcn_exp2f(x[i][j] - ref);
+          float e = __builtin_amdgcn_exp2f(fmaf(sc[nt][i][j], kc, shift));
+          if (masked) e = sc[nt][i][j] == -__builtin_inff() ? 0.0f : e;
           sum += e;
           w[nt][i >> 1][4 * (i & 1) + j] = (_Float16)e;
         }
@@ -229,7 +250,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 
 #pragma unroll
     for (int n = 0; n < NV; n++) {
-      uint4 v = ld_global16(vp + (int64_t)16 * n * T);
+      uint4 v = HOIST ? vr[n] : ld_global16(vp + (int64_t)16 * n * T);
       if (masked) {
         // codes of unwritten positions may be anything, NaN included
         uint32_t a[4] = {v.x, v.y, v.z, v.w};
@@ -330,44 +351,67 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
   }
 }
 
-// Joins the context splits of a row and query head: one wave each, the rows
-// of a tile in turn.
+// Joins the context splits of one row and query head, one workgroup each: the
+// lanes take the splits' maxima and sums, then each wave adds up every fourth
+// split's partial sums, eight loads in flight.
 template <int D, int M>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
+__global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p, BatchView rows) {
   constexpr int E = D >= 64 ? D / 64 : 1;                 // dimensions of a lane
+  __shared__ float s_y[kWaves][D], s_f[kMaxSplits];
+  __shared__ float s_top[kWaves], s_sum[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t H = p.c.heads, h = blockIdx.x % H;
-  const int G = (int)p.group;
+  const int G = (int)p.group, Hq = (int)p.c.heads * G;
+  const int head = (int)(blockIdx.x % Hq);
+  const Seq seq = seq_of_unit(rows, blockIdx.x / Hq);
   Tile t;
-  if (!make_tile(p, blockIdx.x / H, M, t)) return;
-  const int64_t slots = (int64_t)p.b.n_rows * H * G;
-  for (int r = t.row0 + wave; r < min(t.rows, t.row0 + M); r += 4) {
-    const int row = t.s.r0 + r / G, head = (int)h * G + r % G;
-    const int64_t at0 = (int64_t)row * H * G + head;
-    const float* ml = p.ws + p.splits * slots * D;
-    float top = -__builtin_inff();
-    for (uint32_t s = 0; s < p.splits; s++) top = fmaxf(top, ml[(s * slots + at0) * 2]);
-    float l = 0.0f, y[E] = {};
-    for (uint32_t s = 0; s < p.splits; s++) {
-      const int64_t at = s * slots + at0;
-      const float m = ml[at * 2], sum = ml[at * 2 + 1];
-      if (sum == 0.0f) continue;
-      const float f = __builtin_amdgcn_exp2f(m - top);
-      l = fmaf(sum, f, l);
-      if (lane < D / E)
+  const int64_t r = (int64_t)seq.unit * G + head % G;
+  if (!make_tile(p, seq, r / M * M, M, t) || r >= t.rows) return;
+  const int n = t.end > t.begin ? min((int)((t.end - t.begin + (int64_t)p.chunk - 1) / p.chunk), (int)p.splits) : 1;
+  const int64_t slots = (int64_t)p.b.n_rows * Hq;
+  const int64_t at0 = (int64_t)(seq.r0 + (int)seq.unit) * Hq + head;
+  const float* ml = p.ws + p.splits * slots * D + at0 * 2;
+  float top = -__builtin_inff();
+  for (int s = threadIdx.x; s < n; s += 64 * kWaves) top = fmaxf(top, ml[s * slots * 2]);
+  top = wave_fmax(top);
+  if (lane == 0) s_top[wave] = top;
+  __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; e++) y[e] = fmaf(p.ws[at * D + lane * E + e], f, y[e]);
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
-    if (lane < D / E)
-#pragma unroll
-      for (int e = 0; e < E; e++)
-        dst[lane * E + e] = (uint16_t)(p.dtype == KVC_BF16 ? pack2<KVC_BF16>(y[e] * inv, 0.0f)
-                                                           : pack2<KVC_FP16>(y[e] * inv, 0.0f));
-    if (p.lse && lane == 0)
-      p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+  for (int w = 0; w < kWaves; w++) top = fmaxf(top, s_top[w]);
+  float sum = 0.0f;
+  for (int s = threadIdx.x; s < n; s += 64 * kWaves) {
+    const float m = ml[s * slots * 2], l = ml[s * slots * 2 + 1];
+    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);   // a split that saw nothing has sum 0
+    s_f[s] = f;
+    sum += l == 0.0f ? 0.0f : l * f;
   }
+  sum = wave_fsum(sum);
+  if (lane == 0) s_sum[wave] = sum;
+  __syncthreads();
+  float l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; w++) l += s_sum[w];
+  float y[E] = {};
+  const float* acc = p.ws + at0 * D + (lane < D / E ? lane * E : 0);
+#pragma unroll 8
+  for (int s = wave; s < n; s += kWaves) {
+    const float f = s_f[s];
+#pragma unroll
+    for (int e = 0; e < E; e++) y[e] = fmaf(acc[s * slots * D + e], f, y[e]);
+  }
+  if (lane < D / E)
+#pragma unroll
+    for (int e = 0; e < E; e++) s_y[wave][lane * E + e] = y[e];
+  __syncthreads();
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* dst = p.out.data + (int64_t)(seq.r0 + (int)seq.unit) * p.out.stride_row + (int64_t)head * p.out.stride_head;
+  for (int d = threadIdx.x; d < D; d += 64 * kWaves) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) v += s_y[w][d];
+    dst[d] = (uint16_t)(p.dtype == KVC_BF16 ? pack2<KVC_BF16>(v * inv, 0.0f) : pack2<KVC_FP16>(v * inv, 0.0f));
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
 template <int D, int NT>
@@ -377,7 +421,7 @@ hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t strea
   else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.splits > 1) {
-    attend_join_kernel<D, 16 * NT><<<p.units * p.c.heads, 256, 0, stream>>>(p);
+    attend_join_kernel<D, 16 * NT><<<p.join_units * p.c.heads * p.group, 64 * kWaves, 0, stream>>>(p, p.join);
     e = hipGetLastError();
   }
   return e;

@@ -51,7 +51,10 @@ struct AttendParams {
   float scale_log2;                         // softmax scale * log2(e)
   uint32_t units;                           // row tiles
   uint32_t splits, chunk;                   // context splits of `chunk` tokens each
+  BatchView join;                           // splits > 1: units are rows
+  uint32_t join_units;
 };
+constexpr uint32_t kMaxSplits = 2048;
 
 // Launchers.  Weak, so that the host half links without the kernels, as the
 // tests of its argument checks build it; a call then reports KVC_E_HIP.

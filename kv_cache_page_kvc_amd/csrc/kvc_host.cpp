@@ -801,25 +801,30 @@ kvc_status rows_call(kvc_ctx* ctx, const kvc_cache* c, const kvc_batch* b, const
 // of a group), and context splits of `chunk` positions where the tiles alone
 // do not fill the device.
 struct AttendPlan {
-  BatchView b;
-  uint64_t units = 0;
+  BatchView b, join;
+  uint64_t units = 0, join_units = 0;
   uint32_t rows = 16, splits = 1, chunk = 0;
   size_t workspace = 0;
 };
-constexpr uint64_t kAttendGroups = 1024;     // workgroups that fill 256 CUs
+constexpr uint64_t kAttendGroups = 4096;     // workgroups that fill 256 CUs, several times over
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
-  const uint64_t most = (uint64_t)std::min(b->max_rows, b->n_rows) * G;
+  const uint64_t most_rows = std::min(b->max_rows, b->n_rows), most = most_rows * G;
   p->rows = most <= 16 ? 16 : 32;
   p->b = batch_view(b, std::max<uint64_t>(1, (most + p->rows - 1) / p->rows), G, p->rows, 1, &p->units);
+  p->join = batch_view(b, std::max<uint64_t>(1, most_rows), 1, 1, 0, &p->join_units);
   const uint64_t groups = p->units * c->kv_heads;
+  // most positions that one tile's rows see, from a multiple of 64 on
+  uint64_t span = b->max_len;
+  if (o->window && (o->flags & KVC_ATTEND_CAUSAL))
+    span = std::min<uint64_t>(span, (uint64_t)o->window + p->rows / G + 1 + 64);
   uint64_t splits = groups ? (kAttendGroups + groups - 1) / groups : 1;
-  splits = std::min<uint64_t>(splits, (b->max_len + kAttendChunk - 1) / kAttendChunk);
+  splits = std::min<uint64_t>({splits, (span + kAttendChunk - 1) / kAttendChunk, kMaxSplits});
   splits = std::max<uint64_t>(splits, 1);
-  p->chunk = (uint32_t)align_up((b->max_len + splits - 1) / splits, kAttendChunk);
-  p->splits = std::max<uint32_t>(1, p->chunk ? (uint32_t)((b->max_len + p->chunk - 1) / p->chunk) : 1);
-  if (groups * p->splits > 0x7FFFFFFFull) return KVC_E_ARG;
+  p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
+  p->splits = (uint32_t)std::max<uint64_t>(1, (span + p->chunk - 1) / p->chunk);
+  if (groups * p->splits > 0x7FFFFFFFull || p->join_units * o->q_heads > 0x7FFFFFFFull) return KVC_E_ARG;
   p->workspace = p->splits == 1 ? 0 : (size_t)p->splits * b->n_rows * o->q_heads * (c->head_dim + 2) * sizeof(float);
   return KVC_OK;
 }
@@ -1291,6 +1296,8 @@ kvc_status kvc_cache_attend(kvc_ctx* ctx, const kvc_cache* cache, const kvc_batc
     P.units = (uint32_t)plan.units;
     P.splits = plan.splits;
     P.chunk = plan.chunk;
+    P.join = plan.join;
+    P.join_units = (uint32_t)plan.join_units;
     DeviceGuard g(ctx->device);
     if (!g.ok) return KVC_E_HIP;
     const hipError_t e =
