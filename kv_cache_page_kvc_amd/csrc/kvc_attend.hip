@@ -2,7 +2,7 @@
 //
 // For a query row i and the positions j it sees, with the page scales ks, vs:
 //   t_ij = log2(e) * scale * ks[page(j)] * <q_i, kcode_j> + log2(vs[page(j)])
-//   w_ij = 2^(t_ij - m_i),  m_i the running maximum of t_ij minus 15
+//   w_ij = 2^(t_ij - m_i),  m_i 12 below a running reference of the t_ij
 //   out_i = sum_j w_ij vcode_j / sum_j w_ij / vs[page(j)].
 // Folding log2(vs) into the exponent makes w the weight of a *code*: V's codes
 // then enter the product as they are, and w <= 2^15 is a binary16 value
@@ -11,7 +11,7 @@
 // exactly, a query row is scaled by a power of two to a largest |q| in
 // [2^14, 2^15), which keeps every BF16 or FP16 value above 2^-29 of that
 // exact, and the weights are rounded to 11 significant bits (off by 2^-11 of
-// themselves at most, and by 2^-40 of the largest where they are below 2^-29
+// themselves at most, and by 2^-37 of the largest where they are below 2^-26
 // of it).  The denominator, the maxima and the merged sums are binary32.
 //
 // Registers instead of LDS.  A wave takes 64 positions at a time as 4 groups
@@ -30,7 +30,10 @@ namespace {
 
 constexpr int kTile = 64;             // positions a wave takes at a time
 constexpr int kWaves = 4;             // waves of a workgroup
-constexpr float kShift = 15.0f;       // weights are at most 2^15
+// A row's reference m is within kSlack below the largest t seen so far, so
+// weights are at most 2^(kShift + kSlack), a binary16 value, and sums need a
+// new reference only when t has grown by more than kSlack.
+constexpr float kShift = 12.0f, kSlack = 3.5f;
 // Page scales below this count as this: an empty page's scale may be 0.  The
 // scale rule gives at least 1e-12 / 448.
 constexpr float kMinScale = 0x1p-64f;
@@ -55,6 +58,17 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi) {
     }
   }
   return r.v;
+}
+
+// bytes [0, n) of 16, the others 0
+__device__ __forceinline__ uint4 first_bytes(uint4 v, int n) {
+  uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int k = n - 4 * i;
+    a[i] = k >= 4 ? a[i] : (k <= 0 ? 0u : a[i] & ((1u << (8 * k)) - 1u));
+  }
+  return make_uint4(a[0], a[1], a[2], a[3]);
 }
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
@@ -84,6 +98,94 @@ __device__ __forceinline__ bool make_tile(const AttendParams& p, const Seq& s, i
   return true;
 }
 
+// Query row r (token * group + head) of KV head h as the second operand of
+// the score product, this lane's share: the row scaled by a power of two,
+// `crow` what its scores then have to be multiplied with (negative: the row
+// has a NaN or an infinity, and so no finite softmax), `pos` its position
+// (kNowhere: no such row, which sees nothing).
+constexpr int kNowhere = -0x40000001;   // below every position; a window less than 2^30 can be taken off it
+template <int D>
+__device__ __forceinline__ void load_query(const AttendParams& p, const Tile& t, uint32_t h, int r, f16x8* q,
+                                           float& crow, int& pos) {
+  constexpr int KS = D / 32;
+  const int lane = threadIdx.x & 63, g = lane >> 4, G = (int)p.group, i = r / G;
+  const bool in = r < t.rows;
+  pos = in ? t.s.start + i : kNowhere;
+  const uint16_t* qp = p.q.data + (int64_t)(t.s.r0 + i) * p.q.stride_row + (int64_t)(h * G + r % G) * p.q.stride_head;
+  float x[KS][8];
+  float am = 0.0f;
+  bool odd = false;
+#pragma unroll
+  for (int ks = 0; ks < KS; ks++) {
+    const int d = D >= 64 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 8 * g;
+    const uint4 w = in ? ld_global16(qp + d) : make_uint4(0, 0, 0, 0);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const f32x2 f = p.dtype == KVC_BF16 ? unpack2<KVC_BF16>(a[j]) : unpack2<KVC_FP16>(a[j]);
+      x[ks][2 * j] = f.x;
+      x[ks][2 * j + 1] = f.y;
+      odd = odd || !(fabsf(f.x) < __builtin_inff()) || !(fabsf(f.y) < __builtin_inff());
+      am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+  }
+  am = max_across_groups(am);
+  const bool bad = max_across_groups(odd ? 1.0f : 0.0f) != 0.0f;
+  const int e = am > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(am) : 0;
+#pragma unroll
+  for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) q[ks][j] = (_Float16)(bad ? 0.0f : ldexpf(x[ks][j], e));
+  crow = bad ? -1.0f : ldexpf(p.scale_log2, -e);
+}
+// whether a row at `pos` sees position j of the sequence (j is below its length)
+__device__ __forceinline__ bool sees(const AttendParams& p, int pos, int j) {
+  // selects, not branches
+  return (pos != kNowhere) & ((p.causal == 0) | (j <= pos)) & ((p.window == 0) | (j > pos - (int)p.window));
+}
+
+// What a score of this lane's group is multiplied with.  It is kept positive,
+// so that the -infinity of a hidden score stays one whatever the scales are.
+__device__ __forceinline__ float score_factor(float ks, float crow) {
+  return fmaxf(ks * fabsf(crow), 0x1p-126f);
+}
+
+// The row's result: o holds dimensions 16 n + 4 g .. + 3, m and l are the row's.
+template <int D>
+__device__ __forceinline__ void store_row(const AttendParams& p, const Tile& t, uint32_t h, int split, int r,
+                                          const f32x4* o, float crow, float m, float l) {
+  constexpr int NV = D / 16;
+  if (r >= t.rows) return;
+  if (crow < 0.0f && l != 0.0f) l = __builtin_nanf("");
+  const int g = (threadIdx.x & 63) >> 4, G = (int)p.group, Hq = (int)p.c.heads * G;
+  const int row = t.s.r0 + r / G, head = (int)h * G + r % G;
+  if (p.splits > 1) {
+    const int64_t slots = (int64_t)p.b.n_rows * Hq;      // (row, query head) pairs of a split
+    const int64_t at = split * slots + (int64_t)row * Hq + head;
+    float* acc = p.ws + at * D;
+#pragma unroll
+    for (int n = 0; n < NV; n++) *(f32x4*)(acc + 16 * n + 4 * g) = o[n];
+    if (g == 0) {
+      float* ml = p.ws + p.splits * slots * D + at * 2;
+      ml[0] = m;
+      ml[1] = l;
+    }
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
+#pragma unroll
+  for (int n = 0; n < NV; n++) {
+    const f32x4 y = o[n] * inv;
+    const uint2 w = p.dtype == KVC_BF16 ? make_uint2(pack2<KVC_BF16>(y[0], y[1]), pack2<KVC_BF16>(y[2], y[3]))
+                                        : make_uint2(pack2<KVC_FP16>(y[0], y[1]), pack2<KVC_FP16>(y[2], y[3]));
+    st_global8(dst + 16 * n + 4 * g, w);
+  }
+  if (p.lse && g == 0)
+    p.lse[(int64_t)row * Hq + head] =
+        l == 0.0f ? -__builtin_inff() : (m - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+}
+
 // D: head size; NT: tile of 16 * NT query rows, the same for the workgroup's
 // four waves, which take the context's tiles in turn and are joined in LDS.
 template <int D, int NT, uint32_t CODEC>
@@ -98,49 +200,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
   Tile t;
   const Seq seq = seq_of_unit(p.b, rest / p.splits);
   if (!make_tile(p, seq, (int64_t)seq.unit * M, M, t)) return;
-  const int T = 1 << p.c.tshift, G = (int)p.group;
+  const int T = 1 << p.c.tshift;
   // this split's positions; the first one also stands for a tile that sees nothing
   const int64_t from0 = t.begin + (int64_t)split * p.chunk;
   if (split && from0 >= t.end) return;
   const int lo = (int)(from0 / kTile), hi = (int)min((int64_t)t.end, from0 + p.chunk);
 
-  // query rows, scaled by a power of two
   f16x8 q[NT][KS];
   float crow[NT], m[NT], l[NT];
-  int from[NT], to[NT];
+  int pos[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    const int r = t.row0 + 16 * nt + c, i = r / G;
-    const bool in = r < t.rows;
-    from[nt] = p.window ? t.s.start + i - (int)p.window + 1 : 0;
-    to[nt] = in ? (p.causal ? min(t.s.len, t.s.start + i + 1) : t.s.len) : 0;
-    const uint16_t* qp = p.q.data + (int64_t)(t.s.r0 + i) * p.q.stride_row + (int64_t)(h * G + r % G) * p.q.stride_head;
-    float x[KS][8];
-    float am = 0.0f;
-    bool odd = false;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++) {
-      const int d = D >= 64 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 8 * g;
-      const uint4 w = in ? ld_global16(qp + d) : make_uint4(0, 0, 0, 0);
-      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const f32x2 f = p.dtype == KVC_BF16 ? unpack2<KVC_BF16>(a[j]) : unpack2<KVC_FP16>(a[j]);
-        x[ks][2 * j] = f.x;
-        x[ks][2 * j + 1] = f.y;
-        odd = odd || !(fabsf(f.x) < __builtin_inff()) || !(fabsf(f.y) < __builtin_inff());
-        am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    am = max_across_groups(am);
-    const float bad = max_across_groups(odd ? 1.0f : 0.0f);
-    const int e = am > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(am) : 0;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-      for (int j = 0; j < 8; j++) q[nt][ks][j] = (_Float16)(bad != 0.0f ? 0.0f : ldexpf(x[ks][j], e));
-    // a row with an infinity or a NaN has no finite softmax
-    crow[nt] = bad != 0.0f ? __builtin_nanf("") : ldexpf(p.scale_log2, -e);
+    load_query<D>(p, t, h, t.row0 + 16 * nt + c, q[nt], crow[nt], pos[nt]);
     m[nt] = -__builtin_inff();
     l[nt] = 0.0f;
   }
@@ -215,20 +286,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     f16x8 w[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-      const float kc = ks * crow[nt];                       // not negative
+      const float kc = score_factor(ks, crow[nt]);
       if (masked)
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
           for (int j = 0; j < 4; j++) {
-            const int off = 4 * i + j, pos = base + 16 * g + off;
-            sc[nt][i][j] = pos >= from[nt] && pos < to[nt] && off < valid ? sc[nt][i][j] : -__builtin_inff();
+            const int off = 4 * i + j;
+            sc[nt][i][j] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][i][j] : -__builtin_inff();
           }
       float mx = sc[nt][0][0];
 #pragma unroll
       for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[nt][e >> 2][e & 3]);
-      mx = mx == -__builtin_inff() ? mx : fmaf(mx, kc, lvs);   // kc may be 0
-      const float now = fmaxf(m[nt], max_across_groups(mx));
+      const float now = fmaxf(m[nt], max_across_groups(fmaf(mx, kc, lvs)));
       const float ref = now == -__builtin_inff() ? 0.0f : now - kShift;   // a row that has seen nothing yet
       const float keep = now == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
       m[nt] = now;
@@ -238,8 +308,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
       for (int i = 0; i < 4; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          float e = __builtin_amdgcn_exp2f(fmaf(sc[nt][i][j], kc, shift));
-          if (masked) e = sc[nt][i][j] == -__builtin_inff() ? 0.0f : e;
+          const float e = __builtin_amdgcn_exp2f(fmaf(sc[nt][i][j], kc, shift));
           sum += e;
           w[nt][i >> 1][4 * (i & 1) + j] = (_Float16)e;
         }
@@ -251,16 +320,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       uint4 v = HOIST ? vr[n] : ld_global16(vp + (int64_t)16 * n * T);
-      if (masked) {
-        // codes of unwritten positions may be anything, NaN included
-        uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int k = valid - 4 * i;
-          a[i] = k >= 4 ? a[i] : (k <= 0 ? 0u : a[i] & ((1u << (8 * k)) - 1u));
-        }
-        v = make_uint4(a[0], a[1], a[2], a[3]);
-      }
+      if (masked) v = first_bytes(v, valid);   // codes of unwritten positions may be anything, NaN included
       const f16x8 a0 = codes_f16<CODEC>(v.x, v.y), a1 = codes_f16<CODEC>(v.z, v.w);
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) {
@@ -318,37 +378,215 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     __syncthreads();
   }
   if (wave != 0) return;
-  const int64_t slots = (int64_t)p.b.n_rows * H * G;     // (row, query head) pairs of a split
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) store_row<D>(p, t, h, split, t.row0 + 16 * nt + c, o[nt], crow[nt], m[nt], l[nt]);
+}
+
+// Many rows: every wave of the workgroup has 16 * NT rows of its own, and the
+// context's tiles go through LDS, converted to binary16 once for the four
+// waves.  LDS holds operand fragments in the order the lanes read them (64
+// lanes x 16 bytes each), so neither side has bank conflicts; while a tile is
+// worked on, the codes of the next one are on their way into registers, and
+// they are converted into the other half of the buffer.
+template <int D, int NT, uint32_t CODEC, int OCC>
+__global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendParams p) {
+  constexpr int M = 16 * NT * kWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
+  constexpr int VW = (NV + kWaves - 1) / kWaves;             // V fragments' loads of a wave
+  __shared__ uint4 s_k[2][4 * KS][64], s_v[2][NV * 2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  // the last tiles see most (causal): they go first
+  const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
+  const int split = (int)(rest % p.splits);
+  Tile t;
+  const Seq seq = seq_of_unit(p.b, p.units - 1 - rest / p.splits);
+  if (!make_tile(p, seq, (int64_t)seq.unit * M, M, t)) return;
+  const int T = 1 << p.c.tshift, G = (int)p.group;
+  const int64_t from0 = t.begin + (int64_t)split * p.chunk;
+  if (split && from0 >= t.end) return;
+  const int lo = (int)(from0 / kTile), hi = (int)min((int64_t)t.end, from0 + p.chunk);
+
+  f16x8 q[NT][KS];
+  float crow[NT], m[NT], l[NT];
+  int pos[NT];
+  const int row0 = t.row0 + 16 * NT * wave;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    const int r = t.row0 + 16 * nt + c;
-    if (r >= t.rows) continue;
-    const int row = t.s.r0 + r / G, head = (int)h * G + r % G;
-    if (p.splits > 1) {
-      const int64_t at = split * slots + (int64_t)row * H * G + head;
-      float* acc = p.ws + at * D;
-#pragma unroll
-      for (int n = 0; n < NV; n++) *(f32x4*)(acc + 16 * n + 4 * g) = o[nt][n];
-      if (g == 0) {
-        float* ml = p.ws + p.splits * slots * D + at * 2;
-        ml[0] = m[nt];
-        ml[1] = l[nt];
-      }
-      continue;
-    }
-    const float inv = l[nt] == 0.0f ? 0.0f : 1.0f / l[nt];
-    uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
-#pragma unroll
-    for (int n = 0; n < NV; n++) {
-      const f32x4 y = o[nt][n] * inv;
-      const uint2 w = p.dtype == KVC_BF16 ? make_uint2(pack2<KVC_BF16>(y[0], y[1]), pack2<KVC_BF16>(y[2], y[3]))
-                                          : make_uint2(pack2<KVC_FP16>(y[0], y[1]), pack2<KVC_FP16>(y[2], y[3]));
-      st_global8(dst + 16 * n + 4 * g, w);
-    }
-    if (p.lse && g == 0)
-      p.lse[(int64_t)row * H * G + head] =
-          l[nt] == 0.0f ? -__builtin_inff() : (m[nt] - kShift + __builtin_amdgcn_logf(l[nt])) * 0.693147180559945309f;
+    load_query<D>(p, t, h, row0 + 16 * nt + c, q[nt], crow[nt], pos[nt]);
+    m[nt] = -__builtin_inff();
+    l[nt] = 0.0f;
   }
+  f32x4 o[NT][NV];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+    for (int n = 0; n < NV; n++) o[nt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // positions that some, and that every, row of the wave sees
+  const int first = t.s.start + row0 / G, last = t.s.start + min(t.rows - 1, row0 + 16 * NT - 1) / G;
+  const bool any_row = row0 < t.rows;
+  const int w_begin = p.window ? first - (int)p.window + 1 : 0, w_from = p.window ? last - (int)p.window + 1 : 0;
+  const int w_end = any_row ? (p.causal ? last + 1 : t.s.len) : 0, w_to = p.causal ? first + 1 : t.s.len;
+
+  const int32_t* table = p.b.table + (int64_t)t.s.b * p.b.stride_table;
+  const int last_group = (t.s.len - 1) >> 4;
+  bool bad_page = false;
+  auto page_ids = [&](int tile, int32_t& v, int32_t& k) {
+    v = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
+    k = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
+  };
+  // this wave's share of a tile's codes, and the scales of this lane's group
+  uint4 kr[CH], vr[VW];
+  float ks_in, vs_in;
+  int valid_in;
+  auto load_codes = [&](int tile, int32_t pv, int32_t pk) {
+    const bool okv = pv >= 0 && (uint32_t)pv < p.c.num_pages, okk = pk >= 0 && (uint32_t)pk < p.c.num_pages;
+    bad_page = bad_page || !okv;
+    pv = okv ? pv : 0;
+    pk = okk ? pk : 0;
+    const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
+    const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
+    const uint8_t* kp = p.c.k_codes + pk * p.c.stride_page + (int64_t)h * T * D + (gk + 4 * wave + (c & 3)) * D;
+    const uint8_t* vp = p.c.v_codes + pv * p.c.stride_page + (int64_t)h * T * D + c * T + gv;
+#pragma unroll
+    for (int ch = 0; ch < CH; ch++) {
+      if constexpr (D >= 64) {
+        kr[ch] = ld_global16(kp + 64 * ch + 16 * g);
+      } else {
+        const uint2 w = ld_global8(kp + 8 * g);
+        kr[ch] = make_uint4(w.x, w.y, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VW; i++)
+      if (NV % kWaves == 0 || wave + kWaves * i < NV) vr[i] = ld_global16(vp + (int64_t)16 * (wave + kWaves * i) * T);
+    ks_in = p.c.k_scales[pv * p.c.stride_scale + h];
+    vs_in = p.c.v_scales[pv * p.c.stride_scale + h];
+    valid_in = okv ? min(max(t.s.len - tile * kTile - 16 * g, 0), 16) : 0;
+  };
+  auto store_codes = [&](int buf) {
+#pragma unroll
+    for (int ch = 0; ch < CH; ch++) {
+      *(f16x8*)&s_k[buf][wave * KS + 2 * ch * (D >= 64)][lane] = codes_f16<CODEC>(kr[ch].x, kr[ch].y);
+      if constexpr (D >= 64) *(f16x8*)&s_k[buf][wave * KS + 2 * ch + 1][lane] = codes_f16<CODEC>(kr[ch].z, kr[ch].w);
+    }
+    const bool cut = __any(valid_in < 16);
+#pragma unroll
+    for (int i = 0; i < VW; i++) {
+      if (NV % kWaves != 0 && wave + kWaves * i >= NV) continue;
+      const int n = wave + kWaves * i;
+      uint4 v = vr[i];
+      if (cut) v = first_bytes(v, valid_in);
+      *(f16x8*)&s_v[buf][2 * n][lane] = codes_f16<CODEC>(v.x, v.y);
+      *(f16x8*)&s_v[buf][2 * n + 1][lane] = codes_f16<CODEC>(v.z, v.w);
+    }
+  };
+
+  if (lo * kTile < hi) {
+    int32_t next_v, next_k;
+    page_ids(lo, next_v, next_k);
+    load_codes(lo, next_v, next_k);
+    page_ids(lo + 1, next_v, next_k);
+    store_codes(0);
+    float ks = ks_in, vs = vs_in;
+    int valid = valid_in;
+    load_codes(lo + 1, next_v, next_k);
+    page_ids(lo + 2, next_v, next_k);
+    for (int tile = lo, buf = 0; tile * kTile < hi; tile++, buf ^= 1) {
+      const int base = tile * kTile;
+      __syncthreads();           // this tile's fragments are in place, and the other half is free
+      if (base < w_end && base + kTile > w_begin) {
+        const bool masked = base < w_from || base + kTile > w_to || __any(valid < 16);
+        const float vc = fmaxf(vs, kMinScale), lvs = __builtin_amdgcn_logf(vc), ivs = __builtin_amdgcn_rcpf(vc);
+        float kc[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) kc[nt] = score_factor(ks, crow[nt]);
+        // fragments are read a phase ahead: K's of a half while the other
+        // half's second product runs, V's while its weights are formed
+        f16x8 kf[2 * KS], vf[NV];
+        auto read_k = [&](int hh) {
+#pragma unroll
+          for (int s = 0; s < 2 * KS; s++) kf[s] = *(const f16x8*)&s_k[buf][2 * hh * KS + s][lane];
+        };
+        read_k(0);
+#pragma unroll
+        for (int hh = 0; hh < 2; hh++) {
+          f32x4 sc[NT][2];
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              sc[nt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int s = 0; s < KS; s++) sc[nt][i] = mfma(kf[i * KS + s], q[nt][s], sc[nt][i]);
+            }
+#pragma unroll
+          for (int n = 0; n < NV; n++) vf[n] = *(const f16x8*)&s_v[buf][2 * n + hh][lane];
+          __builtin_amdgcn_sched_barrier(0);
+          if (masked)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const int off = 8 * hh + e;
+                sc[nt][e >> 2][e & 3] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][e >> 2][e & 3]
+                                                                                               : -__builtin_inff();
+              }
+          float mx[NT];
+          bool grown = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            float x = sc[nt][0][0];
+#pragma unroll
+            for (int e = 1; e < 8; e++) x = fmaxf(x, sc[nt][e >> 2][e & 3]);
+            mx[nt] = max_across_groups(fmaf(x, kc[nt], lvs));
+            grown |= mx[nt] > m[nt] + kSlack;
+          }
+          if (__any(grown)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              const float now = fmaxf(m[nt], mx[nt]);
+              const float keep = now == m[nt] ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
+              m[nt] = now;
+              l[nt] *= keep;
+#pragma unroll
+              for (int n = 0; n < NV; n++) o[nt][n] *= keep;
+            }
+          }
+          f16x8 w[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            const float shift = lvs - (m[nt] == -__builtin_inff() ? 0.0f : m[nt] - kShift);
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+              const float y = __builtin_amdgcn_exp2f(fmaf(sc[nt][e >> 2][e & 3], kc[nt], shift));
+              sum += y;
+              w[nt][e] = (_Float16)y;
+            }
+            l[nt] = fmaf(sum, ivs, l[nt]);
+          }
+          if (hh == 0) read_k(1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int n = 0; n < NV; n++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) o[nt][n] = mfma(vf[n], w[nt], o[nt][n]);
+        }
+      }
+      if (base + kTile < hi) {
+        store_codes(buf ^ 1);
+        ks = ks_in;
+        vs = vs_in;
+        valid = valid_in;
+        load_codes(tile + 2, next_v, next_k);
+        page_ids(tile + 3, next_v, next_k);
+      }
+    }
+  }
+  if (__any(bad_page)) flag_seq(p.b, t.s.b, KVC_SEQ_BAD_PAGE);
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++)
+    store_row<D>(p, t, h, split, row0 + 16 * nt + c, o[nt], crow[nt], m[nt], sum_across_groups(l[nt]));
 }
 
 // Joins the context splits of one row and query head, one workgroup each: the
@@ -414,21 +652,31 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p
     p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
-template <int D, int NT>
+template <int D, int NT, int ROWS_OCC>
 hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t stream) {
+  constexpr int M = ROWS_OCC ? 16 * NT * kWaves : 16 * NT;
   const dim3 grid(p.units * p.splits * p.c.heads);
-  if (codec == C_FP8) attend_kernel<D, NT, C_FP8><<<grid, 64 * kWaves, 0, stream>>>(p);
-  else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
+  if constexpr (ROWS_OCC) {
+    if (codec == C_FP8) attend_rows_kernel<D, NT, C_FP8, ROWS_OCC><<<grid, 64 * kWaves, 0, stream>>>(p);
+    else attend_rows_kernel<D, NT, C_INT8, ROWS_OCC><<<grid, 64 * kWaves, 0, stream>>>(p);
+  } else {
+    if (codec == C_FP8) attend_kernel<D, NT, C_FP8><<<grid, 64 * kWaves, 0, stream>>>(p);
+    else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
+  }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.splits > 1) {
-    attend_join_kernel<D, 16 * NT><<<p.join_units * p.c.heads * p.group, 64 * kWaves, 0, stream>>>(p, p.join);
+    attend_join_kernel<D, M><<<p.join_units * p.c.heads * p.group, 64 * kWaves, 0, stream>>>(p, p.join);
     e = hipGetLastError();
   }
   return e;
 }
 template <int D>
 hipError_t launch_tile(const AttendParams& p, uint32_t codec, uint32_t rows, hipStream_t stream) {
-  return rows == 16 ? launch_codec<D, 1>(p, codec, stream) : launch_codec<D, 2>(p, codec, stream);
+  constexpr int NT = attend_rows_nt(D);
+  if (rows == 16) return launch_codec<D, 1, 0>(p, codec, stream);
+  if (rows == 32) return launch_codec<D, 2, 0>(p, codec, stream);
+  if (rows == 64 * NT) return launch_codec<D, NT, D == 256 ? 1 : 2>(p, codec, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
