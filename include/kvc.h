@@ -390,7 +390,8 @@ kvc_status kvc_encode_pages_noalloc(const kvc_layout *layout, const kvc_codec *c
  * KVC_E_UNSUPPORTED).  stride_page: bytes between pages of k_codes and of
  * v_codes, a multiple of 16, at least kv_heads * tokens_per_page * head_dim;
  * stride_scale: floats between pages of k_scales and of v_scales, at least
- * kv_heads.  Code pointers are 16-byte aligned, scale pointers 4-byte. */
+ * kv_heads; both below 2^32 (else KVC_E_UNSUPPORTED).  Code pointers are
+ * 16-byte aligned, scale pointers 4-byte. */
 typedef struct {
   uint32_t abi;                 /* KVC_ABI_VERSION */
   uint32_t codec;

@@ -2,7 +2,7 @@
 //
 // For a query row i and the positions j it sees, with the page scales ks, vs:
 //   t_ij = log2(e) * scale * ks[page(j)] * <q_i, kcode_j> + log2(vs[page(j)])
-//   w_ij = 2^(t_ij - m_i),  m_i 12 below a running reference of the t_ij
+//   w_ij = 2^(t_ij - m_i),  m_i 4 below a running reference of the t_ij
 //   out_i = sum_j w_ij vcode_j / sum_j w_ij / vs[page(j)].
 // Folding log2(vs) into the exponent makes w the weight of a *code*: V's codes
 // then enter the product as they are, and w <= 2^15 is a binary16 value
@@ -11,7 +11,7 @@
 // exactly, a query row is scaled by a power of two to a largest |q| in
 // [2^14, 2^15), which keeps every BF16 or FP16 value above 2^-29 of that
 // exact, and the weights are rounded to 11 significant bits (off by 2^-11 of
-// themselves at most, and by 2^-37 of the largest where they are below 2^-26
+// themselves at most, and by 2^-29 of the largest where they are below 2^-18
 // of it).  The denominator, the maxima and the merged sums are binary32.
 //
 // Registers instead of LDS.  A wave takes 64 positions at a time as 4 groups
@@ -32,8 +32,12 @@ constexpr int kTile = 64;             // positions a wave takes at a time
 constexpr int kWaves = 4;             // waves of a workgroup
 // A row's reference m is within kSlack below the largest t seen so far, so
 // weights are at most 2^(kShift + kSlack), a binary16 value, and sums need a
-// new reference only when t has grown by more than kSlack.
-constexpr float kShift = 12.0f, kSlack = 3.5f;
+// new reference only when t has grown by more than kSlack.  Below 2^-14 a
+// weight is rounded to a multiple of 2^-24, at most 2^-29 of the largest off:
+// 2^-12 for a context of 131,072.  (kShift = 12, kSlack = 3.5 raised the
+// reference in a fifth of the half tiles of an 8192-token prompt and cost 4%.)
+constexpr float kShift = 4.0f, kSlack = 11.5f;
+constexpr _Float16 kMostWeight = 46336.0f;   // 2^15.5
 // Page scales below this count as this: an empty page's scale may be 0.  The
 // scale rule gives at least 1e-12 / 448.
 constexpr float kMinScale = 0x1p-64f;
@@ -224,6 +228,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
   const int32_t* table = p.b.table + (int64_t)t.s.b * p.b.stride_table;
   const int last_group = (t.s.len - 1) >> 4;
   bool bad_page = false;
+  const uint8_t* k_lane = p.c.k_codes + (uint64_t)h * T * D + (c & 3) * D + (D >= 64 ? 16 * g : 8 * g);
+  const uint8_t* v_lane = p.c.v_codes + (uint64_t)h * T * D + c * T;
   // page ids of a tile: of this lane's group (scores, V) and of the group of its K rows
   auto page_ids = [&](int tile, int32_t& v, int32_t& k) {
     v = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
@@ -241,25 +247,25 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     pk = okk ? pk : 0;
     const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
     const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
-    const uint8_t* kp = p.c.k_codes + pk * p.c.stride_page + (int64_t)h * T * D + (gk + (c & 3)) * D;
-    const uint8_t* vp = p.c.v_codes + pv * p.c.stride_page + (int64_t)h * T * D + c * T + gv;
+    const uint8_t* kp = k_lane + ((uint64_t)(uint32_t)pk * p.c.stride_page + (uint32_t)(gk * D));
+    const uint8_t* vp = v_lane + ((uint64_t)(uint32_t)pv * p.c.stride_page + (uint32_t)gv);
     uint4 kr[4][CH], vr[NV];
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int ch = 0; ch < CH; ch++) {
         if constexpr (D >= 64) {
-          kr[i][ch] = ld_global16(kp + 4 * i * D + 64 * ch + 16 * g);
+          kr[i][ch] = ld_global16(kp + 4 * i * D + 64 * ch);
         } else {
-          const uint2 w = ld_global8(kp + 4 * i * D + 8 * g);
+          const uint2 w = ld_global8(kp + 4 * i * D);
           kr[i][ch] = make_uint4(w.x, w.y, 0, 0);
         }
       }
-    const float ks = p.c.k_scales[pv * p.c.stride_scale + h];
-    const float vs = fmaxf(p.c.v_scales[pv * p.c.stride_scale + h], kMinScale);
+    const uint64_t at = (uint64_t)(uint32_t)pv * p.c.stride_scale + h;
+    const float ks = p.c.k_scales[at], vs = fmaxf(p.c.v_scales[at], kMinScale);
     if constexpr (HOIST)
 #pragma unroll
-      for (int n = 0; n < NV; n++) vr[n] = ld_global16(vp + (int64_t)16 * n * T);
+      for (int n = 0; n < NV; n++) vr[n] = ld_global16(vp + 16 * n * T);
     const int valid = okv ? min(max(t.s.len - base - 16 * g, 0), 16) : 0;   // positions of the group that are written
     const float lvs = __builtin_amdgcn_logf(vs), ivs = __builtin_amdgcn_rcpf(vs);
 
@@ -319,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 
 #pragma unroll
     for (int n = 0; n < NV; n++) {
-      uint4 v = HOIST ? vr[n] : ld_global16(vp + (int64_t)16 * n * T);
+      uint4 v = HOIST ? vr[n] : ld_global16(vp + 16 * n * T);
       if (masked) v = first_bytes(v, valid);   // codes of unwritten positions may be anything, NaN included
       const f16x8 a0 = codes_f16<CODEC>(v.x, v.y), a1 = codes_f16<CODEC>(v.z, v.w);
 #pragma unroll
@@ -435,6 +441,8 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
     k = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
   };
   // this wave's share of a tile's codes, and the scales of this lane's group
+  const uint8_t* k_lane = p.c.k_codes + (uint64_t)h * T * D + (4 * wave + (c & 3)) * D + (D >= 64 ? 16 * g : 8 * g);
+  const uint8_t* v_lane = p.c.v_codes + (uint64_t)h * T * D + (16 * wave + c) * T;
   uint4 kr[CH], vr[VW];
   float ks_in, vs_in;
   int valid_in;
@@ -445,22 +453,23 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
     pk = okk ? pk : 0;
     const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
     const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
-    const uint8_t* kp = p.c.k_codes + pk * p.c.stride_page + (int64_t)h * T * D + (gk + 4 * wave + (c & 3)) * D;
-    const uint8_t* vp = p.c.v_codes + pv * p.c.stride_page + (int64_t)h * T * D + c * T + gv;
+    const uint8_t* kp = k_lane + ((uint64_t)(uint32_t)pk * p.c.stride_page + (uint32_t)(gk * D));
+    const uint8_t* vp = v_lane + ((uint64_t)(uint32_t)pv * p.c.stride_page + (uint32_t)gv);
 #pragma unroll
     for (int ch = 0; ch < CH; ch++) {
       if constexpr (D >= 64) {
-        kr[ch] = ld_global16(kp + 64 * ch + 16 * g);
+        kr[ch] = ld_global16(kp + 64 * ch);
       } else {
-        const uint2 w = ld_global8(kp + 8 * g);
+        const uint2 w = ld_global8(kp);
         kr[ch] = make_uint4(w.x, w.y, 0, 0);
       }
     }
 #pragma unroll
     for (int i = 0; i < VW; i++)
-      if (NV % kWaves == 0 || wave + kWaves * i < NV) vr[i] = ld_global16(vp + (int64_t)16 * (wave + kWaves * i) * T);
-    ks_in = p.c.k_scales[pv * p.c.stride_scale + h];
-    vs_in = p.c.v_scales[pv * p.c.stride_scale + h];
+      if (NV % kWaves == 0 || wave + kWaves * i < NV) vr[i] = ld_global16(vp + 16 * kWaves * i * T);
+    const uint64_t at = (uint64_t)(uint32_t)pv * p.c.stride_scale + h;
+    ks_in = p.c.k_scales[at];
+    vs_in = p.c.v_scales[at];
     valid_in = okv ? min(max(t.s.len - tile * kTile - 16 * g, 0), 16) : 0;
   };
   auto store_codes = [&](int buf) {
@@ -500,6 +509,13 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
         float kc[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) kc[nt] = score_factor(ks, crow[nt]);
+        // A tile whose positions every row sees, once every row has a reference:
+        // the weights are formed against it as it is, and only if one of them
+        // is too large for binary16 is it raised.  Else the maximum comes first.
+        bool first = masked;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) first |= m[nt] == -__builtin_inff();
+        first = __any(first);
         // fragments are read a phase ahead: K's of a half while the other
         // half's second product runs, V's while its weights are formed
         f16x8 kf[2 * KS], vf[NV];
@@ -522,49 +538,68 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
 #pragma unroll
           for (int n = 0; n < NV; n++) vf[n] = *(const f16x8*)&s_v[buf][2 * n + hh][lane];
           __builtin_amdgcn_sched_barrier(0);
-          if (masked)
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const int off = 8 * hh + e;
-                sc[nt][e >> 2][e & 3] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][e >> 2][e & 3]
-                                                                                               : -__builtin_inff();
-              }
-          float mx[NT];
-          bool grown = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            float x = sc[nt][0][0];
-#pragma unroll
-            for (int e = 1; e < 8; e++) x = fmaxf(x, sc[nt][e >> 2][e & 3]);
-            mx[nt] = max_across_groups(fmaf(x, kc[nt], lvs));
-            grown |= mx[nt] > m[nt] + kSlack;
-          }
-          if (__any(grown)) {
+          f16x8 w[NT];
+          float sum[NT];
+          auto weigh = [&]() {
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-              const float now = fmaxf(m[nt], mx[nt]);
+              const float shift = lvs - (m[nt] - kShift);
+              sum[nt] = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const float y = __builtin_amdgcn_exp2f(fmaf(sc[nt][e >> 2][e & 3], kc[nt], shift));
+                sum[nt] += y;
+                w[nt][e] = (_Float16)y;
+              }
+            }
+          };
+          bool raise = first;
+          if (!first) {
+            weigh();
+            f16x2 top = {0, 0};
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              const f16x8 x = w[nt];
+              const f16x2 a = {x[0], x[1]}, b = {x[2], x[3]}, c2 = {x[4], x[5]}, d = {x[6], x[7]};
+              top = __builtin_elementwise_max(top, __builtin_elementwise_max(__builtin_elementwise_max(a, b),
+                                                                             __builtin_elementwise_max(c2, d)));
+            }
+            raise = __any((top[0] > kMostWeight) | (top[1] > kMostWeight));
+          }
+          if (raise) {
+            if (masked)
+#pragma unroll
+              for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                  const int off = 8 * hh + e;
+                  sc[nt][e >> 2][e & 3] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][e >> 2][e & 3]
+                                                                                                 : -__builtin_inff();
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              float x = sc[nt][0][0];
+#pragma unroll
+              for (int e = 1; e < 8; e++) x = fmaxf(x, sc[nt][e >> 2][e & 3]);
+              const float mx = max_across_groups(fmaf(x, kc[nt], lvs)), now = mx > m[nt] + kSlack ? mx : m[nt];
               const float keep = now == m[nt] ? 1.0f : __builtin_amdgcn_exp2f(m[nt] - now);
               m[nt] = now;
               l[nt] *= keep;
 #pragma unroll
               for (int n = 0; n < NV; n++) o[nt][n] *= keep;
             }
-          }
-          f16x8 w[NT];
+            weigh();
+            // a row that has seen nothing yet: 2^(-inf + inf)
 #pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            const float shift = lvs - (m[nt] == -__builtin_inff() ? 0.0f : m[nt] - kShift);
-            float sum = 0.0f;
+            for (int nt = 0; nt < NT; nt++)
+              if (m[nt] == -__builtin_inff()) {
+                sum[nt] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float y = __builtin_amdgcn_exp2f(fmaf(sc[nt][e >> 2][e & 3], kc[nt], shift));
-              sum += y;
-              w[nt][e] = (_Float16)y;
-            }
-            l[nt] = fmaf(sum, ivs, l[nt]);
+                for (int e = 0; e < 8; e++) w[nt][e] = (_Float16)0.0f;
+              }
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) l[nt] = fmaf(sum[nt], ivs, l[nt]);
           if (hh == 0) read_k(1);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -15,7 +15,7 @@ namespace kvc {
 struct CacheView {
   uint8_t *k_codes, *v_codes;               // [page][head][token][D], [page][head][D][token]
   float *k_scales, *v_scales;               // [page][head]
-  int64_t stride_page, stride_scale;        // bytes; floats
+  uint32_t stride_page, stride_scale;       // bytes; floats
   uint32_t num_pages, heads, tshift;        // tokens_per_page = 1 << tshift
 };
 struct BatchView {

@@ -676,10 +676,8 @@ kvc_status check_cache(const kvc_cache* c) {
   if (c->num_pages == 0 || c->num_pages > (uint64_t)std::numeric_limits<int32_t>::max()) return KVC_E_ARG;
   if (c->stride_page < (int64_t)c->kv_heads * T * D || c->stride_page % 16) return KVC_E_ARG;
   if (c->stride_scale < (int64_t)c->kv_heads) return KVC_E_ARG;
-  // the pools' extents stay within 63 bits
-  if (c->stride_page > std::numeric_limits<int64_t>::max() / (int64_t)c->num_pages ||
-      c->stride_scale > std::numeric_limits<int64_t>::max() / 4 / (int64_t)c->num_pages)
-    return KVC_E_ARG;
+  // the kernels multiply page ids with 32-bit strides
+  if (c->stride_page > 0xFFFFFFFFll || c->stride_scale > 0xFFFFFFFFll) return KVC_E_UNSUPPORTED;
   if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return KVC_E_ARG;
   if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & 15) return KVC_E_ARG;
   if (((uintptr_t)c->k_scales | (uintptr_t)c->v_scales) & 3) return KVC_E_ARG;
@@ -734,8 +732,8 @@ CacheView cache_view(const kvc_cache* c) {
   v.v_codes = static_cast<uint8_t*>(c->v_codes);
   v.k_scales = c->k_scales;
   v.v_scales = c->v_scales;
-  v.stride_page = c->stride_page;
-  v.stride_scale = c->stride_scale;
+  v.stride_page = (uint32_t)c->stride_page;
+  v.stride_scale = (uint32_t)c->stride_scale;
   v.num_pages = (uint32_t)c->num_pages;
   v.heads = c->kv_heads;
   while ((1u << v.tshift) < c->tokens_per_page) v.tshift++;

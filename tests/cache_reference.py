@@ -163,10 +163,10 @@ def attend(pool, table, cu, lengths, q, scale, causal, window, hidden_pages=()):
 
 
 # The weights p_j * vs_j of V's codes are held in binary16 with the largest
-# seen so far at 2^12 at least: below 2^-14 they are rounded to multiples of
-# 2^-24, so off by at most 2^-25, which is 2^-37 of the largest, for each
+# seen so far at 2^4 at least: below 2^-14 they are rounded to multiples of
+# 2^-24, so off by at most 2^-25, which is 2^-29 of the largest, for each
 # position.
-SMALLEST_WEIGHT = 2.0 ** -37
+SMALLEST_WEIGHT = 2.0 ** -29
 
 
 def weight_error():

@@ -59,7 +59,7 @@ BAD_CACHES = [
     (dict(tokens_per_page=8), kvc.KVC_E_UNSUPPORTED), (dict(tokens_per_page=48), kvc.KVC_E_UNSUPPORTED),
     (dict(tokens_per_page=512, stride_page=1 << 30), kvc.KVC_E_UNSUPPORTED), (dict(kv_heads=0), kvc.KVC_E_ARG),
     (dict(num_pages=0), kvc.KVC_E_ARG), (dict(num_pages=1 << 31), kvc.KVC_E_ARG), (dict(stride_page=4 * 16 * 128 - 16), kvc.KVC_E_ARG),
-    (dict(stride_page=4 * 16 * 128 + 8), kvc.KVC_E_ARG), (dict(stride_page=1 << 62), kvc.KVC_E_ARG), (dict(stride_scale=3), kvc.KVC_E_ARG),
+    (dict(stride_page=4 * 16 * 128 + 8), kvc.KVC_E_ARG), (dict(stride_page=1 << 32), kvc.KVC_E_UNSUPPORTED), (dict(stride_scale=1 << 32), kvc.KVC_E_UNSUPPORTED), (dict(stride_scale=3), kvc.KVC_E_ARG),
     (dict(k_codes=None), kvc.KVC_E_ARG), (dict(v_codes=FAKE + 8), kvc.KVC_E_ARG), (dict(k_scales=FAKE + 2), kvc.KVC_E_ARG),
     (dict(v_scales=None), kvc.KVC_E_ARG),
 ]
