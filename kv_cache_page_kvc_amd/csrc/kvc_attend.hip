@@ -23,6 +23,8 @@
 // weights and both operands stay in registers, a lane's loads are 16
 // consecutive bytes of K (dimensions) and V (positions), and the running
 // maximum needs two lane swaps a row.
+#include <type_traits>
+
 #include "kvc_cache_device.h"
 
 namespace kvc {
@@ -79,6 +81,14 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Workgroup barrier for LDS only: __syncthreads would also wait for the global
+// loads in flight, which are registers of their own wave.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // one row tile of a sequence and KV head
 struct Tile {
   Seq s;
@@ -115,24 +125,37 @@ __device__ __forceinline__ void load_query(const AttendParams& p, const Tile& t,
   const int lane = threadIdx.x & 63, g = lane >> 4, G = (int)p.group, i = r / G;
   const bool in = r < t.rows;
   pos = in ? t.s.start + i : kNowhere;
-  const uint16_t* qp = p.q.data + (int64_t)(t.s.r0 + i) * p.q.stride_row + (int64_t)(h * G + r % G) * p.q.stride_head;
+  // a row that is not there loads the first one's values; all loads go out together
+  const int row = in ? i : 0, head = in ? r - i * G : 0;
+  const uint16_t* qp = p.q.data + (int64_t)(t.s.r0 + row) * p.q.stride_row + (int64_t)((int)h * G + head) * p.q.stride_head;
+  uint4 raw[KS];
+#pragma unroll
+  for (int ks = 0; ks < KS; ks++) raw[ks] = ld_global16(qp + (D >= 64 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 8 * g));
   float x[KS][8];
+  auto unpack = [&](auto dt) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) {
+      const uint32_t a[4] = {raw[ks].x, raw[ks].y, raw[ks].z, raw[ks].w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const f32x2 f = unpack2<decltype(dt)::value>(a[j]);
+        x[ks][2 * j] = f.x;
+        x[ks][2 * j + 1] = f.y;
+      }
+    }
+  };
+  if (p.dtype == KVC_BF16) unpack(std::integral_constant<int, KVC_BF16>{});
+  else unpack(std::integral_constant<int, KVC_FP16>{});
   float am = 0.0f;
   bool odd = false;
 #pragma unroll
-  for (int ks = 0; ks < KS; ks++) {
-    const int d = D >= 64 ? 64 * (ks / 2) + 16 * g + 8 * (ks & 1) : 8 * g;
-    const uint4 w = in ? ld_global16(qp + d) : make_uint4(0, 0, 0, 0);
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+  for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const f32x2 f = p.dtype == KVC_BF16 ? unpack2<KVC_BF16>(a[j]) : unpack2<KVC_FP16>(a[j]);
-      x[ks][2 * j] = f.x;
-      x[ks][2 * j + 1] = f.y;
-      odd = odd || !(fabsf(f.x) < __builtin_inff()) || !(fabsf(f.y) < __builtin_inff());
-      am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+    for (int j = 0; j < 8; j++) {
+      x[ks][j] = in ? x[ks][j] : 0.0f;
+      odd |= !(fabsf(x[ks][j]) < __builtin_inff());
+      am = fmaxf(am, fabsf(x[ks][j]));
     }
-  }
   am = max_across_groups(am);
   const bool bad = max_across_groups(odd ? 1.0f : 0.0f) != 0.0f;
   const int e = am > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(am) : 0;
@@ -178,13 +201,15 @@ __device__ __forceinline__ void store_row(const AttendParams& p, const Tile& t, 
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* dst = p.out.data + (int64_t)row * p.out.stride_row + (int64_t)head * p.out.stride_head;
+  auto put = [&](auto dt) {
 #pragma unroll
-  for (int n = 0; n < NV; n++) {
-    const f32x4 y = o[n] * inv;
-    const uint2 w = p.dtype == KVC_BF16 ? make_uint2(pack2<KVC_BF16>(y[0], y[1]), pack2<KVC_BF16>(y[2], y[3]))
-                                        : make_uint2(pack2<KVC_FP16>(y[0], y[1]), pack2<KVC_FP16>(y[2], y[3]));
-    st_global8(dst + 16 * n + 4 * g, w);
-  }
+    for (int n = 0; n < NV; n++) {
+      const f32x4 y = o[n] * inv;
+      st_global8(dst + 16 * n + 4 * g, make_uint2(pack2<decltype(dt)::value>(y[0], y[1]), pack2<decltype(dt)::value>(y[2], y[3])));
+    }
+  };
+  if (p.dtype == KVC_BF16) put(std::integral_constant<int, KVC_BF16>{});
+  else put(std::integral_constant<int, KVC_FP16>{});
   if (p.lse && g == 0)
     p.lse[(int64_t)row * Hq + head] =
         l == 0.0f ? -__builtin_inff() : (m - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
@@ -399,6 +424,7 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
   constexpr int M = 16 * NT * kWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
   constexpr int VW = (NV + kWaves - 1) / kWaves;             // V fragments' loads of a wave
   __shared__ uint4 s_k[2][4 * KS][64], s_v[2][NV * 2][64];
+  __shared__ float4 s_scale[2][4];     // of each group: K's scale, log2 and reciprocal of V's, written positions
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   // the last tiles see most (causal): they go first
   const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
@@ -478,15 +504,21 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
       *(f16x8*)&s_k[buf][wave * KS + 2 * ch * (D >= 64)][lane] = codes_f16<CODEC>(kr[ch].x, kr[ch].y);
       if constexpr (D >= 64) *(f16x8*)&s_k[buf][wave * KS + 2 * ch + 1][lane] = codes_f16<CODEC>(kr[ch].z, kr[ch].w);
     }
-    const bool cut = __any(valid_in < 16);
+    if (__any(valid_in < 16))
+#pragma unroll
+      for (int i = 0; i < VW; i++) vr[i] = first_bytes(vr[i], valid_in);
 #pragma unroll
     for (int i = 0; i < VW; i++) {
       if (NV % kWaves != 0 && wave + kWaves * i >= NV) continue;
       const int n = wave + kWaves * i;
-      uint4 v = vr[i];
-      if (cut) v = first_bytes(v, valid_in);
-      *(f16x8*)&s_v[buf][2 * n][lane] = codes_f16<CODEC>(v.x, v.y);
-      *(f16x8*)&s_v[buf][2 * n + 1][lane] = codes_f16<CODEC>(v.z, v.w);
+      *(f16x8*)&s_v[buf][2 * n][lane] = codes_f16<CODEC>(vr[i].x, vr[i].y);
+      *(f16x8*)&s_v[buf][2 * n + 1][lane] = codes_f16<CODEC>(vr[i].z, vr[i].w);
+    }
+    // through LDS: as registers carried over the loop, the scales would be
+    // waited for as soon as they were asked for
+    if (wave == 0 && c == 0) {
+      const float vc = fmaxf(vs_in, kMinScale);
+      s_scale[buf][g] = make_float4(ks_in, __builtin_amdgcn_logf(vc), __builtin_amdgcn_rcpf(vc), (float)valid_in);
     }
   };
 
@@ -496,16 +528,16 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
     load_codes(lo, next_v, next_k);
     page_ids(lo + 1, next_v, next_k);
     store_codes(0);
-    float ks = ks_in, vs = vs_in;
-    int valid = valid_in;
     load_codes(lo + 1, next_v, next_k);
     page_ids(lo + 2, next_v, next_k);
     for (int tile = lo, buf = 0; tile * kTile < hi; tile++, buf ^= 1) {
       const int base = tile * kTile;
-      __syncthreads();           // this tile's fragments are in place, and the other half is free
+      lds_barrier();             // this tile's fragments are in place, and the other half is free
       if (base < w_end && base + kTile > w_begin) {
+        const float4 group = s_scale[buf][g];
+        const float ks = group.x, lvs = group.y, ivs = group.z;
+        const int valid = (int)group.w;
         const bool masked = base < w_from || base + kTile > w_to || __any(valid < 16);
-        const float vc = fmaxf(vs, kMinScale), lvs = __builtin_amdgcn_logf(vc), ivs = __builtin_amdgcn_rcpf(vc);
         float kc[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) kc[nt] = score_factor(ks, crow[nt]);
@@ -610,9 +642,6 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
       }
       if (base + kTile < hi) {
         store_codes(buf ^ 1);
-        ks = ks_in;
-        vs = vs_in;
-        valid = valid_in;
         load_codes(tile + 2, next_v, next_k);
         page_ids(tile + 3, next_v, next_k);
       }

@@ -29,7 +29,9 @@ __device__ __forceinline__ void flag_seq(const BatchView& b, uint32_t seq, uint3
 }
 
 __device__ __forceinline__ void load_seq(const BatchView& v, uint32_t b, Seq& s) {
-  const int r0 = v.cu[b], r1 = v.cu[b + 1], len = v.lengths[b];
+  // the wave's own values: what follows from them stays scalar
+  const int r0 = __builtin_amdgcn_readfirstlane(v.cu[b]), r1 = __builtin_amdgcn_readfirstlane(v.cu[b + 1]),
+            len = __builtin_amdgcn_readfirstlane(v.lengths[b]);
   s.b = b;
   s.r0 = r0;
   s.n = r1 - r0;
