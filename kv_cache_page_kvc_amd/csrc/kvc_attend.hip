@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kTile = 64;             // positions a wave takes at a time
 constexpr int kWaves = 4;             // waves of a workgroup
+constexpr int kRowWaves = 8;          // of attend_rows_kernel's
 // A row's reference m is within kSlack below the largest t seen so far, so
 // weights are at most 2^(kShift + kSlack), a binary16 value, and sums need a
 // new reference only when t has grown by more than kSlack.  Below 2^-14 a
@@ -165,10 +166,14 @@ __device__ __forceinline__ void load_query(const AttendParams& p, const Tile& t,
     for (int j = 0; j < 8; j++) q[ks][j] = (_Float16)(bad ? 0.0f : ldexpf(x[ks][j], e));
   crow = bad ? -1.0f : ldexpf(p.scale_log2, -e);
 }
-// whether a row at `pos` sees position j of the sequence (j is below its length)
-__device__ __forceinline__ bool sees(const AttendParams& p, int pos, int j) {
-  // selects, not branches
-  return (pos != kNowhere) & ((p.causal == 0) | (j <= pos)) & ((p.window == 0) | (j > pos - (int)p.window));
+// Of the positions at .. at + 15, of which `valid` are written, a row at `pos`
+// sees at + [lo, hi].
+struct Seen {
+  int lo, hi;
+};
+__device__ __forceinline__ Seen seen(const AttendParams& p, int pos, int at, int valid) {
+  const int rel = pos - at;
+  return {p.window ? rel - (int)p.window + 1 : 0, pos == kNowhere ? -1 : min(valid - 1, p.causal ? rel : 15)};
 }
 
 // What a score of this lane's group is multiplied with.  It is kept positive,
@@ -318,14 +323,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
       const float kc = score_factor(ks, crow[nt]);
-      if (masked)
+      if (masked) {
+        const Seen v = seen(p, pos[nt], base + 16 * g, valid);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const int off = 4 * i + j;
-            sc[nt][i][j] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][i][j] : -__builtin_inff();
-          }
+        for (int e = 0; e < 16; e++)
+          sc[nt][e >> 2][e & 3] = ((e >= v.lo) & (e <= v.hi)) ? sc[nt][e >> 2][e & 3] : -__builtin_inff();
+      }
       float mx = sc[nt][0][0];
 #pragma unroll
       for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[nt][e >> 2][e & 3]);
@@ -414,18 +417,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 }
 
 // Many rows: every wave of the workgroup has 16 * NT rows of its own, and the
-// context's tiles go through LDS, converted to binary16 once for the four
+// context's tiles go through LDS, converted to binary16 once for the eight
 // waves.  LDS holds operand fragments in the order the lanes read them (64
 // lanes x 16 bytes each), so neither side has bank conflicts; while a tile is
 // worked on, the codes of the next one are on their way into registers, and
-// they are converted into the other half of the buffer.
-template <int D, int NT, uint32_t CODEC, int OCC>
-__global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendParams p) {
-  constexpr int M = 16 * NT * kWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
-  constexpr int VW = (NV + kWaves - 1) / kWaves;             // V fragments' loads of a wave
-  __shared__ uint4 s_k[2][4 * KS][64], s_v[2][NV * 2][64];
+// they are converted into the other half of the buffer.  Waves 0 .. 3 stage
+// the tile's K, each one product tile of 16 positions, waves 4 .. 7 its V.
+template <int D, int NT, uint32_t CODEC>
+__global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendParams p) {
+  constexpr int M = 16 * NT * kRowWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
+  constexpr int V0 = 4 * KS;           // V's fragments come behind K's
+  __shared__ uint4 s_f[2][V0 + 2 * NV][64];
   __shared__ float4 s_scale[2][4];     // of each group: K's scale, log2 and reciprocal of V's, written positions
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), part = wave & 3;
+  const bool of_v = wave >= 4, idle = of_v && part >= NV;
   // the last tiles see most (causal): they go first
   const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
   const int split = (int)(rest % p.splits);
@@ -462,74 +468,68 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
   const int32_t* table = p.b.table + (int64_t)t.s.b * p.b.stride_table;
   const int last_group = (t.s.len - 1) >> 4;
   bool bad_page = false;
-  auto page_ids = [&](int tile, int32_t& v, int32_t& k) {
-    v = table[(16 * min(4 * tile + g, last_group)) >> p.c.tshift];
-    k = table[(16 * min(4 * tile + (c >> 2), last_group)) >> p.c.tshift];
-  };
+  // this lane's group of a tile: of its K rows' positions, or of its V columns' (and of its scores')
+  const int my_group = of_v ? g : c >> 2;
+  auto page_id = [&](int tile) { return table[(16 * min(4 * tile + my_group, last_group)) >> p.c.tshift]; };
   // this wave's share of a tile's codes, and the scales of this lane's group
-  const uint8_t* k_lane = p.c.k_codes + (uint64_t)h * T * D + (4 * wave + (c & 3)) * D + (D >= 64 ? 16 * g : 8 * g);
-  const uint8_t* v_lane = p.c.v_codes + (uint64_t)h * T * D + (16 * wave + c) * T;
-  uint4 kr[CH], vr[VW];
-  float ks_in, vs_in;
-  int valid_in;
-  auto load_codes = [&](int tile, int32_t pv, int32_t pk) {
-    const bool okv = pv >= 0 && (uint32_t)pv < p.c.num_pages, okk = pk >= 0 && (uint32_t)pk < p.c.num_pages;
-    bad_page = bad_page || !okv;
-    pv = okv ? pv : 0;
-    pk = okk ? pk : 0;
-    const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
-    const int gk = (16 * min(4 * tile + (c >> 2), last_group)) & (T - 1);
-    const uint8_t* kp = k_lane + ((uint64_t)(uint32_t)pk * p.c.stride_page + (uint32_t)(gk * D));
-    const uint8_t* vp = v_lane + ((uint64_t)(uint32_t)pv * p.c.stride_page + (uint32_t)gv);
+  uint4 raw[CH];
+  float ks_in = 0.0f, vs_in = 0.0f;
+  int valid_in = 16;
+  const uint8_t* lane_codes = of_v ? p.c.v_codes + (uint64_t)h * T * D + (uint32_t)((16 * part + c) * T)
+                                   : p.c.k_codes + (uint64_t)h * T * D + (4 * part + (c & 3)) * D + (D >= 64 ? 16 : 8) * g;
+  const uint32_t token_bytes = of_v ? 1 : D, step = of_v ? 64 * T : 64;
+  auto load_codes = [&](int tile, int32_t id) {
+    if (idle) return;
+    const bool ok = (uint32_t)id < p.c.num_pages;
+    const uint32_t page = ok ? (uint32_t)id : 0u;
+    const uint32_t at = (uint32_t)(16 * min(4 * tile + my_group, last_group)) & (T - 1);
+    const uint8_t* src = lane_codes + ((uint64_t)page * p.c.stride_page + at * token_bytes);
 #pragma unroll
     for (int ch = 0; ch < CH; ch++) {
-      if constexpr (D >= 64) {
-        kr[ch] = ld_global16(kp + 64 * ch);
+      if (D >= 64 || of_v) {
+        raw[ch] = ld_global16(src + ch * step);
       } else {
-        const uint2 w = ld_global8(kp);
-        kr[ch] = make_uint4(w.x, w.y, 0, 0);
+        const uint2 w = ld_global8(src);
+        raw[ch] = make_uint4(w.x, w.y, 0, 0);
       }
     }
-#pragma unroll
-    for (int i = 0; i < VW; i++)
-      if (NV % kWaves == 0 || wave + kWaves * i < NV) vr[i] = ld_global16(vp + 16 * kWaves * i * T);
-    const uint64_t at = (uint64_t)(uint32_t)pv * p.c.stride_scale + h;
-    ks_in = p.c.k_scales[at];
-    vs_in = p.c.v_scales[at];
-    valid_in = okv ? min(max(t.s.len - tile * kTile - 16 * g, 0), 16) : 0;
+    if (of_v) {
+      bad_page = bad_page || !ok;
+      valid_in = ok ? min(max(t.s.len - tile * kTile - 16 * g, 0), 16) : 0;
+      if (part == 0) {
+        const uint64_t i = (uint64_t)page * p.c.stride_scale + h;
+        ks_in = p.c.k_scales[i];
+        vs_in = p.c.v_scales[i];
+      }
+    }
   };
   auto store_codes = [&](int buf) {
+    if (idle) return;
+    if (of_v && __any(valid_in < 16))
+#pragma unroll
+      for (int ch = 0; ch < CH; ch++) raw[ch] = first_bytes(raw[ch], valid_in);
 #pragma unroll
     for (int ch = 0; ch < CH; ch++) {
-      *(f16x8*)&s_k[buf][wave * KS + 2 * ch * (D >= 64)][lane] = codes_f16<CODEC>(kr[ch].x, kr[ch].y);
-      if constexpr (D >= 64) *(f16x8*)&s_k[buf][wave * KS + 2 * ch + 1][lane] = codes_f16<CODEC>(kr[ch].z, kr[ch].w);
-    }
-    if (__any(valid_in < 16))
-#pragma unroll
-      for (int i = 0; i < VW; i++) vr[i] = first_bytes(vr[i], valid_in);
-#pragma unroll
-    for (int i = 0; i < VW; i++) {
-      if (NV % kWaves != 0 && wave + kWaves * i >= NV) continue;
-      const int n = wave + kWaves * i;
-      *(f16x8*)&s_v[buf][2 * n][lane] = codes_f16<CODEC>(vr[i].x, vr[i].y);
-      *(f16x8*)&s_v[buf][2 * n + 1][lane] = codes_f16<CODEC>(vr[i].z, vr[i].w);
+      // fragments of K: chunk by chunk of the positions' dimensions; of V: every fourth 16 dimensions
+      const int slot = of_v ? V0 + 2 * (part + 4 * ch) : part * KS + (D >= 64 ? 2 * ch : 0);
+      *(f16x8*)&s_f[buf][slot][lane] = codes_f16<CODEC>(raw[ch].x, raw[ch].y);
+      if (D >= 64 || of_v) *(f16x8*)&s_f[buf][slot + 1][lane] = codes_f16<CODEC>(raw[ch].z, raw[ch].w);
     }
     // through LDS: as registers carried over the loop, the scales would be
     // waited for as soon as they were asked for
-    if (wave == 0 && c == 0) {
+    if (wave == 4 && c == 0) {
       const float vc = fmaxf(vs_in, kMinScale);
       s_scale[buf][g] = make_float4(ks_in, __builtin_amdgcn_logf(vc), __builtin_amdgcn_rcpf(vc), (float)valid_in);
     }
   };
 
   if (lo * kTile < hi) {
-    int32_t next_v, next_k;
-    page_ids(lo, next_v, next_k);
-    load_codes(lo, next_v, next_k);
-    page_ids(lo + 1, next_v, next_k);
+    int32_t next = page_id(lo);
+    load_codes(lo, next);
+    next = page_id(lo + 1);
     store_codes(0);
-    load_codes(lo + 1, next_v, next_k);
-    page_ids(lo + 2, next_v, next_k);
+    load_codes(lo + 1, next);
+    next = page_id(lo + 2);
     for (int tile = lo, buf = 0; tile * kTile < hi; tile++, buf ^= 1) {
       const int base = tile * kTile;
       lds_barrier();             // this tile's fragments are in place, and the other half is free
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
         f16x8 kf[2 * KS], vf[NV];
         auto read_k = [&](int hh) {
 #pragma unroll
-          for (int s = 0; s < 2 * KS; s++) kf[s] = *(const f16x8*)&s_k[buf][2 * hh * KS + s][lane];
+          for (int s = 0; s < 2 * KS; s++) kf[s] = *(const f16x8*)&s_f[buf][2 * hh * KS + s][lane];
         };
         read_k(0);
 #pragma unroll
@@ -568,8 +568,7 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
               for (int s = 0; s < KS; s++) sc[nt][i] = mfma(kf[i * KS + s], q[nt][s], sc[nt][i]);
             }
 #pragma unroll
-          for (int n = 0; n < NV; n++) vf[n] = *(const f16x8*)&s_v[buf][2 * n + hh][lane];
-          __builtin_amdgcn_sched_barrier(0);
+          for (int n = 0; n < NV; n++) vf[n] = *(const f16x8*)&s_f[buf][V0 + 2 * n + hh][lane];
           f16x8 w[NT];
           float sum[NT];
           auto weigh = [&]() {
@@ -601,13 +600,12 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
           if (raise) {
             if (masked)
 #pragma unroll
-              for (int nt = 0; nt < NT; nt++)
+              for (int nt = 0; nt < NT; nt++) {
+                const Seen v = seen(p, pos[nt], base + 16 * g + 8 * hh, valid - 8 * hh);
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                  const int off = 8 * hh + e;
-                  sc[nt][e >> 2][e & 3] = (sees(p, pos[nt], base + 16 * g + off) & (off < valid)) ? sc[nt][e >> 2][e & 3]
-                                                                                                 : -__builtin_inff();
-                }
+                for (int e = 0; e < 8; e++)
+                  sc[nt][e >> 2][e & 3] = ((e >= v.lo) & (e <= v.hi)) ? sc[nt][e >> 2][e & 3] : -__builtin_inff();
+              }
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
               float x = sc[nt][0][0];
@@ -633,7 +631,6 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) l[nt] = fmaf(sum[nt], ivs, l[nt]);
           if (hh == 0) read_k(1);
-          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int n = 0; n < NV; n++)
 #pragma unroll
@@ -642,8 +639,8 @@ __global__ __launch_bounds__(64 * kWaves, OCC) void attend_rows_kernel(AttendPar
       }
       if (base + kTile < hi) {
         store_codes(buf ^ 1);
-        load_codes(tile + 2, next_v, next_k);
-        page_ids(tile + 3, next_v, next_k);
+        load_codes(tile + 2, next);
+        next = page_id(tile + 3);
       }
     }
   }
@@ -716,13 +713,13 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p
     p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
-template <int D, int NT, int ROWS_OCC>
+template <int D, int NT, bool ROWS>
 hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t stream) {
-  constexpr int M = ROWS_OCC ? 16 * NT * kWaves : 16 * NT;
+  constexpr int M = 16 * NT * (ROWS ? kRowWaves : 1);
   const dim3 grid(p.units * p.splits * p.c.heads);
-  if constexpr (ROWS_OCC) {
-    if (codec == C_FP8) attend_rows_kernel<D, NT, C_FP8, ROWS_OCC><<<grid, 64 * kWaves, 0, stream>>>(p);
-    else attend_rows_kernel<D, NT, C_INT8, ROWS_OCC><<<grid, 64 * kWaves, 0, stream>>>(p);
+  if constexpr (ROWS) {
+    if (codec == C_FP8) attend_rows_kernel<D, NT, C_FP8><<<grid, 64 * kRowWaves, 0, stream>>>(p);
+    else attend_rows_kernel<D, NT, C_INT8><<<grid, 64 * kRowWaves, 0, stream>>>(p);
   } else {
     if (codec == C_FP8) attend_kernel<D, NT, C_FP8><<<grid, 64 * kWaves, 0, stream>>>(p);
     else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
@@ -736,10 +733,10 @@ hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t strea
 }
 template <int D>
 hipError_t launch_tile(const AttendParams& p, uint32_t codec, uint32_t rows, hipStream_t stream) {
-  constexpr int NT = attend_rows_nt(D);
-  if (rows == 16) return launch_codec<D, 1, 0>(p, codec, stream);
-  if (rows == 32) return launch_codec<D, 2, 0>(p, codec, stream);
-  if (rows == 64 * NT) return launch_codec<D, NT, D == 256 ? 1 : 2>(p, codec, stream);
+  constexpr int M = attend_tile_rows(D);
+  if (rows == 16) return launch_codec<D, 1, false>(p, codec, stream);
+  if (rows == 32) return launch_codec<D, 2, false>(p, codec, stream);
+  if (rows == M) return launch_codec<D, M / (16 * kRowWaves), true>(p, codec, stream);
   return hipErrorInvalidValue;
 }
 

@@ -55,9 +55,9 @@ struct AttendParams {
   uint32_t join_units;
 };
 constexpr uint32_t kMaxSplits = 2048;
-// Query rows of a tile, in 64s, where the workgroup's four waves have rows of
-// their own (attend_rows_kernel).
-constexpr int attend_rows_nt(int d) { return d >= 128 ? 2 : 4; }
+// Query rows of a tile where the workgroup's eight waves have rows of their
+// own (attend_rows_kernel).
+constexpr int attend_tile_rows(int d) { return d == 256 ? 128 : 256; }
 
 // Launchers.  Weak, so that the host half links without the kernels, as the
 // tests of its argument checks build it; a call then reports KVC_E_HIP.

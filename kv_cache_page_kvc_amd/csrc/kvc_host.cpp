@@ -805,14 +805,14 @@ struct AttendPlan {
   size_t workspace = 0;
 };
 // Workgroups that fill 256 CUs: few rows (a tile's four waves share the
-// context) want many, for even shares of ragged lengths; with many rows two a
-// CU are resident and every split costs a pass over its rows' partial sums.
-constexpr uint64_t kAttendGroups = 4096, kAttendRowsGroups = 512;
+// context) want many, for even shares of ragged lengths; with many rows one a
+// CU is resident and every split costs a pass over its rows' partial sums.
+constexpr uint64_t kAttendGroups = 4096, kAttendRowsGroups = 256;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
   const uint64_t most_rows = std::min(b->max_rows, b->n_rows), most = most_rows * G;
-  p->rows = most <= 16 ? 16 : (most <= 32 ? 32 : 64 * attend_rows_nt((int)c->head_dim));
+  p->rows = most <= 16 ? 16 : (most <= 32 ? 32 : attend_tile_rows((int)c->head_dim));
   p->b = batch_view(b, std::max<uint64_t>(1, (most + p->rows - 1) / p->rows), G, p->rows, 1, &p->units);
   p->join = batch_view(b, std::max<uint64_t>(1, most_rows), 1, 1, 0, &p->join_units);
   const uint64_t groups = p->units * c->kv_heads;
