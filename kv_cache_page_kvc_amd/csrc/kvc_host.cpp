@@ -786,7 +786,7 @@ kvc_status rows_call(kvc_ctx* ctx, const kvc_cache* c, const kvc_batch* b, const
   P.k = rows_view(k);
   P.v = rows_view(v);
   P.units = (uint32_t)units;
-  if (units * c->kv_heads * 2 / 4 >= 0x7FFFFFFFull) return KVC_E_ARG;
+  if (units * c->kv_heads * 2 * (T / 16) >= 0x7FFFFFFFull) return KVC_E_ARG;
   if (!(write ? launch_cache_write : launch_cache_read)) return KVC_E_HIP;
   DeviceGuard g(ctx->device);
   if (!g.ok) return KVC_E_HIP;
