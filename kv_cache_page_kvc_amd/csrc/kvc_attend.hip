@@ -650,14 +650,14 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
     store_row<D>(p, t, h, split, row0 + 16 * nt + c, o[nt], crow[nt], m[nt], sum_across_groups(l[nt]));
 }
 
-// Joins the context splits of one row and query head, one workgroup each: the
-// lanes take the splits' maxima and sums, then each wave adds up every fourth
-// split's partial sums, eight loads in flight.
-template <int D, int M>
-__global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p, BatchView rows) {
+// Joins the context splits of one row and query head, one workgroup of WAVES
+// each: the lanes take the splits' maxima and sums, then each wave adds up its
+// share of the splits' partial sums, eight loads in flight.
+template <int D, int M, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attend_join_kernel(AttendParams p, BatchView rows) {
   constexpr int E = D >= 64 ? D / 64 : 1;                 // dimensions of a lane
-  __shared__ float s_y[kWaves][D], s_f[kMaxSplits];
-  __shared__ float s_top[kWaves], s_sum[kWaves];
+  __shared__ float s_y[WAVES][D], s_f[kMaxSplits];
+  __shared__ float s_top[WAVES], s_sum[WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int G = (int)p.group, Hq = (int)p.c.heads * G;
   const int head = (int)(blockIdx.x % Hq);
@@ -670,14 +670,14 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p
   const int64_t at0 = (int64_t)(seq.r0 + (int)seq.unit) * Hq + head;
   const float* ml = p.ws + p.splits * slots * D + at0 * 2;
   float top = -__builtin_inff();
-  for (int s = threadIdx.x; s < n; s += 64 * kWaves) top = fmaxf(top, ml[s * slots * 2]);
+  for (int s = threadIdx.x; s < n; s += 64 * WAVES) top = fmaxf(top, ml[s * slots * 2]);
   top = wave_fmax(top);
   if (lane == 0) s_top[wave] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; w++) top = fmaxf(top, s_top[w]);
+  for (int w = 0; w < WAVES; w++) top = fmaxf(top, s_top[w]);
   float sum = 0.0f;
-  for (int s = threadIdx.x; s < n; s += 64 * kWaves) {
+  for (int s = threadIdx.x; s < n; s += 64 * WAVES) {
     const float m = ml[s * slots * 2], l = ml[s * slots * 2 + 1];
     const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);   // a split that saw nothing has sum 0
     s_f[s] = f;
@@ -688,11 +688,11 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p
   __syncthreads();
   float l = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; w++) l += s_sum[w];
+  for (int w = 0; w < WAVES; w++) l += s_sum[w];
   float y[E] = {};
   const float* acc = p.ws + at0 * D + (lane < D / E ? lane * E : 0);
 #pragma unroll 8
-  for (int s = wave; s < n; s += kWaves) {
+  for (int s = wave; s < n; s += WAVES) {
     const float f = s_f[s];
 #pragma unroll
     for (int e = 0; e < E; e++) y[e] = fmaf(acc[s * slots * D + e], f, y[e]);
@@ -703,10 +703,10 @@ __global__ __launch_bounds__(64 * kWaves) void attend_join_kernel(AttendParams p
   __syncthreads();
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint16_t* dst = p.out.data + (int64_t)(seq.r0 + (int)seq.unit) * p.out.stride_row + (int64_t)head * p.out.stride_head;
-  for (int d = threadIdx.x; d < D; d += 64 * kWaves) {
+  for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) v += s_y[w][d];
+    for (int w = 0; w < WAVES; w++) v += s_y[w][d];
     dst[d] = (uint16_t)(p.dtype == KVC_BF16 ? pack2<KVC_BF16>(v * inv, 0.0f) : pack2<KVC_FP16>(v * inv, 0.0f));
   }
   if (p.lse && threadIdx.x == 0)
@@ -726,7 +726,10 @@ hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t strea
   }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.splits > 1) {
-    attend_join_kernel<D, M><<<p.join_units * p.c.heads * p.group, 64 * kWaves, 0, stream>>>(p, p.join);
+    // many splits of few rows are a latency: sixteen waves a row took 5 us where four took 11 (256 splits)
+    const uint32_t grid = p.join_units * p.c.heads * p.group;
+    if (p.splits > 16) attend_join_kernel<D, M, 16><<<grid, 1024, 0, stream>>>(p, p.join);
+    else attend_join_kernel<D, M, 4><<<grid, 256, 0, stream>>>(p, p.join);
     e = hipGetLastError();
   }
   return e;

@@ -136,8 +136,10 @@ __global__ __launch_bounds__(item_waves(T) == 8 ? 512 : 256) void cache_write_ke
   const int lt = lane / LPT, ld = (lane % LPT) * 8;
   const int part = V::PARTS == 1 ? 0 : lane / (D / 2), vd = 2 * (lane % (D / 2 < 64 ? D / 2 : 64));
 
-  // the rows, into registers
-  uint32_t x[REGS];
+  const bool fresh = q0 == 0;
+  const float old = fresh || !work ? 0.0f : *scale;            // before any wave sets it, below
+  // the rows, into registers, and V's codes beside them where a lane's tokens are not all new
+  uint32_t x[REGS], was[GPW * V::ROUNDS * 2 * (V::TOK / 4)];
   uint32_t am = 0, odd = 0;
 #pragma unroll
   for (int k = 0; k < GPW; k++) {
@@ -159,14 +161,20 @@ __global__ __launch_bounds__(item_waves(T) == 8 ? 512 : 256) void cache_write_ke
         const int t = t0 + part * V::TOK + i % V::TOK, d = vd + 128 * (i / V::TOK);
         x[k * V::ROUNDS * V::TOK + i] = t >= q0 && t < q1 ? ld_global4(src + (int64_t)(t - q0) * rv.stride_row + d) : 0u;
       }
+      const int tl = t0 + part * V::TOK;
+      if (tl < q0 || tl + V::TOK > q1)
+#pragma unroll
+        for (int i = 0; i < V::ROUNDS * 2; i++) {
+          const uint8_t* at = codes + (int64_t)(vd + 128 * (i / 2) + i % 2) * T + tl;
+#pragma unroll
+          for (int j = 0; j < V::TOK / 4; j++) was[(k * V::ROUNDS * 2 + i) * (V::TOK / 4) + j] = ld_global4(at + 4 * j);
+        }
 #pragma unroll
       for (int i = 0; i < V::ROUNDS * V::TOK; i++) pair_max<DT>(x[k * V::ROUNDS * V::TOK + i], am, odd);
     }
   }
   am = wave_umax(am);
   odd = __any((int)odd) ? 1u : 0u;
-  const bool fresh = q0 == 0;
-  const float old = fresh || !work ? 0.0f : *scale;            // before any wave sets it, below
   if constexpr (WPI > 1) {
     if (lane == 0) {
       s_max[wave] = am;
@@ -221,6 +229,8 @@ __global__ __launch_bounds__(item_waves(T) == 8 ? 512 : 256) void cache_write_ke
           uint32_t now[2][V::TOK / 4];
 #pragma unroll
           for (int j = 0; j < V::TOK; j += 4) {
+            now[0][j / 4] = now[1][j / 4] = 0;
+            if (EXACT && (tl + j + 4 <= q0 || tl + j >= q1)) continue;   // divisions are slow, and single tokens common
             f32x2 y[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) y[i] = unpack2<DT>(some ? xv[j + i] : 0u);
@@ -240,9 +250,9 @@ __global__ __launch_bounds__(item_waves(T) == 8 ? 512 : 256) void cache_write_ke
                 const uint32_t before = low_bytes(q0 - (tl + 4 * j)), upto = low_bytes(q1 - (tl + 4 * j));
                 const uint32_t mine = upto & ~before;
                 if (mine || (EXACT && grown && before)) {
-                  const uint32_t was = *(g_u32*)(at + j);
-                  const uint32_t kept = EXACT && grown ? requant4<CODEC>(was, from, s) : was;
-                  *(g_u32*)(at + j) = (now[i][j] & mine) | (kept & before) | (was & ~(mine | before));
+                  const uint32_t then = some ? was[((k * V::ROUNDS + rd) * 2 + i) * (V::TOK / 4) + j] : ld_global4(at + j);
+                  const uint32_t kept = EXACT && grown ? requant4<CODEC>(then, from, s) : then;
+                  *(g_u32*)(at + j) = (now[i][j] & mine) | (kept & before) | (then & ~(mine | before));
                 }
               }
             }

@@ -804,15 +804,17 @@ struct AttendPlan {
   uint32_t rows = 16, splits = 1, chunk = 0;
   size_t workspace = 0;
 };
-// Workgroups that fill 256 CUs: few rows (a tile's four waves share the
-// context) want many, for even shares of ragged lengths; with many rows one a
-// CU is resident and every split costs a pass over its rows' partial sums.
-constexpr uint64_t kAttendGroups = 4096, kAttendRowsGroups = 256;
+// Context splits, in workgroups of the whole launch.  Few rows (a tile's four
+// waves share the context): at least 768 to fill 256 CUs, shares of 1024
+// positions beyond that to even out ragged lengths, at most 4096 for their
+// join.  Many rows: one workgroup a CU is resident, and every split costs a
+// pass over its rows' partial sums.
+constexpr uint64_t kAttendFill = 768, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
   const uint64_t most_rows = std::min(b->max_rows, b->n_rows), most = most_rows * G;
-  p->rows = most <= 16 ? 16 : (most <= 32 ? 32 : attend_tile_rows((int)c->head_dim));
+  p->rows = most <= 16 ? 16 : (most <= 64 ? 32 : attend_tile_rows((int)c->head_dim));
   p->b = batch_view(b, std::max<uint64_t>(1, (most + p->rows - 1) / p->rows), G, p->rows, 1, &p->units);
   p->join = batch_view(b, std::max<uint64_t>(1, most_rows), 1, 1, 0, &p->join_units);
   const uint64_t groups = p->units * c->kv_heads;
@@ -820,8 +822,12 @@ kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend*
   uint64_t span = b->max_len;
   if (o->window && (o->flags & KVC_ATTEND_CAUSAL))
     span = std::min<uint64_t>(span, (uint64_t)o->window + p->rows / G + 1 + 64);
-  const uint64_t fill = p->rows <= 32 ? kAttendGroups : kAttendRowsGroups;
-  uint64_t splits = groups ? (fill + groups - 1) / groups : 1;
+  uint64_t splits = 1;
+  if (groups && p->rows <= 32)
+    splits = std::min((kAttendMost + groups - 1) / groups,
+                      std::max((kAttendFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare));
+  else if (groups)
+    splits = (kAttendRowsFill + groups - 1) / groups;
   splits = std::min<uint64_t>({splits, (span + kAttendChunk - 1) / kAttendChunk, kMaxSplits});
   splits = std::max<uint64_t>(splits, 1);
   p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
