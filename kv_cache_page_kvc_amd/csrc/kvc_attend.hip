@@ -31,7 +31,7 @@ namespace kvc {
 namespace {
 
 constexpr int kTile = 64;             // positions a wave takes at a time
-constexpr int kWaves = 4;             // waves of a workgroup
+constexpr int kWaves = 4;             // waves of a workgroup of attend_kernel
 constexpr int kRowWaves = 8;          // of attend_rows_kernel's
 // A row's reference m is within kSlack below the largest t seen so far, so
 // weights are at most 2^(kShift + kSlack), a binary16 value, and sums need a
@@ -713,6 +713,56 @@ __global__ __launch_bounds__(64 * WAVES) void attend_join_kernel(AttendParams p,
     p.lse[at0] = l == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
+// The same for few splits, one wave a row and query head: everything it needs
+// is asked for at once, and every lane forms the row's maximum and sum.
+constexpr uint32_t kFewSplits = 16;
+template <int D, int M>
+__global__ __launch_bounds__(256) void attend_join_few_kernel(AttendParams p, BatchView rows) {
+  constexpr int E = D >= 64 ? D / 64 : 1;                 // dimensions of a lane
+  const int lane = threadIdx.x & 63;
+  const int G = (int)p.group, Hq = (int)p.c.heads * G;
+  const uint32_t id = blockIdx.x * 4 + (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (id >= p.join_units * (uint32_t)Hq) return;
+  const int head = (int)(id % Hq);
+  const Seq seq = seq_of_unit(rows, id / Hq);
+  Tile t;
+  const int64_t r = (int64_t)seq.unit * G + head % G;
+  if (!make_tile(p, seq, r / M * M, M, t) || r >= t.rows) return;
+  const int n = t.end > t.begin ? min((int)((t.end - t.begin + (int64_t)p.chunk - 1) / p.chunk), (int)p.splits) : 1;
+  const int64_t slots = (int64_t)p.b.n_rows * Hq, at0 = (int64_t)(seq.r0 + (int)seq.unit) * Hq + head;
+  const float* ml = p.ws + p.splits * slots * D + at0 * 2;
+  const float* acc = p.ws + at0 * D + (lane < D / E ? lane * E : 0);
+  float m[kFewSplits], l[kFewSplits], y[kFewSplits][E];
+#pragma unroll
+  for (int s = 0; s < (int)kFewSplits; s++)
+    if (s < n) {
+      m[s] = ml[s * slots * 2];
+      l[s] = ml[s * slots * 2 + 1];
+#pragma unroll
+      for (int e = 0; e < E; e++) y[s][e] = acc[s * slots * D + e];
+    }
+  float top = -__builtin_inff(), sum = 0.0f, v[E] = {};
+#pragma unroll
+  for (int s = 0; s < (int)kFewSplits; s++)
+    if (s < n) top = fmaxf(top, m[s]);
+#pragma unroll
+  for (int s = 0; s < (int)kFewSplits; s++)
+    if (s < n) {
+      const float f = l[s] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[s] - top);   // a split that saw nothing has sum 0
+      sum += l[s] == 0.0f ? 0.0f : l[s] * f;
+#pragma unroll
+      for (int e = 0; e < E; e++) v[e] = fmaf(y[s][e], f, v[e]);
+    }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* dst = p.out.data + (int64_t)(seq.r0 + (int)seq.unit) * p.out.stride_row + (int64_t)head * p.out.stride_head;
+  if (lane < D / E)
+#pragma unroll
+    for (int e = 0; e < E; e++)
+      dst[lane * E + e] = (uint16_t)(p.dtype == KVC_BF16 ? pack2<KVC_BF16>(v[e] * inv, 0.0f) : pack2<KVC_FP16>(v[e] * inv, 0.0f));
+  if (p.lse && lane == 0)
+    p.lse[at0] = sum == 0.0f ? -__builtin_inff() : (top - kShift + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+}
+
 template <int D, int NT, bool ROWS>
 hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t stream) {
   constexpr int M = 16 * NT * (ROWS ? kRowWaves : 1);
@@ -726,10 +776,9 @@ hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t strea
   }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.splits > 1) {
-    // many splits of few rows are a latency: sixteen waves a row took 5 us where four took 11 (256 splits)
-    const uint32_t grid = p.join_units * p.c.heads * p.group;
-    if (p.splits > 16) attend_join_kernel<D, M, 16><<<grid, 1024, 0, stream>>>(p, p.join);
-    else attend_join_kernel<D, M, 4><<<grid, 256, 0, stream>>>(p, p.join);
+    const uint32_t rows = p.join_units * p.c.heads * p.group;
+    if (p.splits <= kFewSplits) attend_join_few_kernel<D, M><<<(rows + 3) / 4, 256, 0, stream>>>(p, p.join);
+    else attend_join_kernel<D, M, 16><<<rows, 1024, 0, stream>>>(p, p.join);
     e = hipGetLastError();
   }
   return e;

@@ -805,11 +805,11 @@ struct AttendPlan {
   size_t workspace = 0;
 };
 // Context splits, in workgroups of the whole launch.  Few rows (a tile's four
-// waves share the context): at least 768 to fill 256 CUs, shares of 1024
+// waves share the context): at least 512 to fill 256 CUs, shares of 1024
 // positions beyond that to even out ragged lengths, at most 4096 for their
 // join.  Many rows: one workgroup a CU is resident, and every split costs a
 // pass over its rows' partial sums.
-constexpr uint64_t kAttendFill = 768, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
+constexpr uint64_t kAttendFill = 512, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
