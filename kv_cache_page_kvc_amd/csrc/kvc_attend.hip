@@ -427,8 +427,11 @@ template <int D, int NT, uint32_t CODEC>
 __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendParams p) {
   constexpr int M = 16 * NT * kRowWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
   constexpr int V0 = 4 * KS;           // V's fragments come behind K's
-  __shared__ uint4 s_f[2][V0 + 2 * NV][64];
-  __shared__ float4 s_scale[2][4];     // of each group: K's scale, log2 and reciprocal of V's, written positions
+  // A ring of tiles: half of them are worked on between two barriers while
+  // the other half is filled.  Two tiles a barrier where LDS holds four.
+  constexpr int RING = D <= 128 ? 4 : 2, AHEAD = RING / 2;
+  __shared__ uint4 s_f[RING][V0 + 2 * NV][64];
+  __shared__ float4 s_scale[RING][4];  // of each group: K's scale, log2 and reciprocal of V's, written positions
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), part = wave & 3;
   const bool of_v = wave >= 4, idle = of_v && part >= NV;
@@ -525,14 +528,18 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
 
   if (lo * kTile < hi) {
     int32_t next = page_id(lo);
-    load_codes(lo, next);
-    next = page_id(lo + 1);
-    store_codes(0);
-    load_codes(lo + 1, next);
-    next = page_id(lo + 2);
-    for (int tile = lo, buf = 0; tile * kTile < hi; tile++, buf ^= 1) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) {
+      load_codes(lo + i, next);
+      next = page_id(lo + i + 1);
+      store_codes(i);
+    }
+    load_codes(lo + AHEAD, next);
+    next = page_id(lo + AHEAD + 1);
+    for (int tile = lo, buf = 0; tile * kTile < hi; tile++, buf = (buf + 1) % RING) {
       const int base = tile * kTile;
-      lds_barrier();             // this tile's fragments are in place, and the other half is free
+      // the tiles of this half of the ring are in place, and the other half is free
+      if (buf % AHEAD == 0) lds_barrier();
       if (base < w_end && base + kTile > w_begin) {
         const float4 group = s_scale[buf][g];
         const float ks = group.x, lvs = group.y, ivs = group.z;
@@ -637,10 +644,10 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
             for (int nt = 0; nt < NT; nt++) o[nt][n] = mfma(vf[n], w[nt], o[nt][n]);
         }
       }
-      if (base + kTile < hi) {
-        store_codes(buf ^ 1);
-        load_codes(tile + 2, next);
-        next = page_id(tile + 3);
+      if (base + AHEAD * kTile < hi) {
+        store_codes((buf + AHEAD) % RING);
+        load_codes(tile + AHEAD + 1, next);
+        next = page_id(tile + AHEAD + 2);
       }
     }
   }
