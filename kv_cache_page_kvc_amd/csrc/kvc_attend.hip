@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kTile = 64;             // positions a wave takes at a time
 constexpr int kWaves = 4;             // waves of a workgroup of attend_kernel
-constexpr int kRowWaves = 8;          // of attend_rows_kernel's
 // A row's reference m is within kSlack below the largest t seen so far, so
 // weights are at most 2^(kShift + kSlack), a binary16 value, and sums need a
 // new reference only when t has grown by more than kSlack.  Below 2^-14 a
@@ -417,15 +416,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 }
 
 // Many rows: every wave of the workgroup has 16 * NT rows of its own, and the
-// context's tiles go through LDS, converted to binary16 once for the eight
-// waves.  LDS holds operand fragments in the order the lanes read them (64
+// context's tiles go through LDS, converted to binary16 once for all of them.  LDS holds operand fragments in the order the lanes read them (64
 // lanes x 16 bytes each), so neither side has bank conflicts; while a tile is
 // worked on, the codes of the next one are on their way into registers, and
 // they are converted into the other half of the buffer.  Waves 0 .. 3 stage
 // the tile's K, each one product tile of 16 positions, waves 4 .. 7 its V.
+// Twelve waves, three a SIMD, hide each other's latencies best: an 8192-row
+// prompt of 32 heads took 522 us, with eight waves and fragments read a phase
+// ahead 529 (and 519 against 556 for chunks of INT8); at D = 256 the output's
+// registers allow eight.
 template <int D, int NT, uint32_t CODEC>
-__global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendParams p) {
-  constexpr int M = 16 * NT * kRowWaves, KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
+__global__ __launch_bounds__(64 * attend_row_waves(D), attend_row_waves(D) / 4) void attend_rows_kernel(AttendParams p) {
+  constexpr int M = 16 * NT * attend_row_waves(D), KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
   constexpr int V0 = 4 * KS;           // V's fragments come behind K's
   // A ring of tiles: half of them are worked on between two barriers while
   // the other half is filled.  Two tiles a barrier where LDS holds four.
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
   __shared__ float4 s_scale[RING][4];  // of each group: K's scale, log2 and reciprocal of V's, written positions
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), part = wave & 3;
-  const bool of_v = wave >= 4, idle = of_v && part >= NV;
+  const bool of_v = wave >= 4, idle = wave >= 8 || (of_v && part >= NV);
   // the last tiles see most (causal): they go first
   const uint32_t H = p.c.heads, h = blockIdx.x % H, rest = blockIdx.x / H;
   const int split = (int)(rest % p.splits);
@@ -555,27 +557,18 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) first |= m[nt] == -__builtin_inff();
         first = __any(first);
-        // fragments are read a phase ahead: K's of a half while the other
-        // half's second product runs, V's while its weights are formed
-        f16x8 kf[2 * KS], vf[NV];
-        auto read_k = [&](int hh) {
-#pragma unroll
-          for (int s = 0; s < 2 * KS; s++) kf[s] = *(const f16x8*)&s_f[buf][2 * hh * KS + s][lane];
-        };
-        read_k(0);
-#pragma unroll
+#pragma unroll 1
         for (int hh = 0; hh < 2; hh++) {
           f32x4 sc[NT][2];
 #pragma unroll
           for (int i = 0; i < 2; i++)
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-              sc[nt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int s = 0; s < KS; s++) {
+              const f16x8 a = *(const f16x8*)&s_f[buf][(2 * hh + i) * KS + s][lane];
 #pragma unroll
-              for (int s = 0; s < KS; s++) sc[nt][i] = mfma(kf[i * KS + s], q[nt][s], sc[nt][i]);
+              for (int nt = 0; nt < NT; nt++)
+                sc[nt][i] = mfma(a, q[nt][s], s ? sc[nt][i] : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
             }
-#pragma unroll
-          for (int n = 0; n < NV; n++) vf[n] = *(const f16x8*)&s_f[buf][V0 + 2 * n + hh][lane];
           f16x8 w[NT];
           float sum[NT];
           auto weigh = [&]() {
@@ -637,11 +630,12 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void attend_rows_kernel(AttendPa
           }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) l[nt] = fmaf(sum[nt], ivs, l[nt]);
-          if (hh == 0) read_k(1);
 #pragma unroll
-          for (int n = 0; n < NV; n++)
+          for (int n = 0; n < NV; n++) {
+            const f16x8 a = *(const f16x8*)&s_f[buf][V0 + 2 * n + hh][lane];
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++) o[nt][n] = mfma(vf[n], w[nt], o[nt][n]);
+            for (int nt = 0; nt < NT; nt++) o[nt][n] = mfma(a, w[nt], o[nt][n]);
+          }
         }
       }
       if (base + AHEAD * kTile < hi) {
@@ -772,11 +766,11 @@ __global__ __launch_bounds__(256) void attend_join_few_kernel(AttendParams p, Ba
 
 template <int D, int NT, bool ROWS>
 hipError_t launch_codec(const AttendParams& p, uint32_t codec, hipStream_t stream) {
-  constexpr int M = 16 * NT * (ROWS ? kRowWaves : 1);
+  constexpr int M = 16 * NT * (ROWS ? attend_row_waves(D) : 1);
   const dim3 grid(p.units * p.splits * p.c.heads);
   if constexpr (ROWS) {
-    if (codec == C_FP8) attend_rows_kernel<D, NT, C_FP8><<<grid, 64 * kRowWaves, 0, stream>>>(p);
-    else attend_rows_kernel<D, NT, C_INT8><<<grid, 64 * kRowWaves, 0, stream>>>(p);
+    if (codec == C_FP8) attend_rows_kernel<D, NT, C_FP8><<<grid, 64 * attend_row_waves(D), 0, stream>>>(p);
+    else attend_rows_kernel<D, NT, C_INT8><<<grid, 64 * attend_row_waves(D), 0, stream>>>(p);
   } else {
     if (codec == C_FP8) attend_kernel<D, NT, C_FP8><<<grid, 64 * kWaves, 0, stream>>>(p);
     else attend_kernel<D, NT, C_INT8><<<grid, 64 * kWaves, 0, stream>>>(p);
@@ -795,7 +789,7 @@ hipError_t launch_tile(const AttendParams& p, uint32_t codec, uint32_t rows, hip
   constexpr int M = attend_tile_rows(D);
   if (rows == 16) return launch_codec<D, 1, false>(p, codec, stream);
   if (rows == 32) return launch_codec<D, 2, false>(p, codec, stream);
-  if (rows == M) return launch_codec<D, M / (16 * kRowWaves), true>(p, codec, stream);
+  if (rows == M) return launch_codec<D, M / (16 * attend_row_waves(D)), true>(p, codec, stream);
   return hipErrorInvalidValue;
 }
 

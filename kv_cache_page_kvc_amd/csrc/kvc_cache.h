@@ -55,9 +55,10 @@ struct AttendParams {
   uint32_t join_units;
 };
 constexpr uint32_t kMaxSplits = 2048;
-// Query rows of a tile where the workgroup's eight waves have rows of their
-// own (attend_rows_kernel).
-constexpr int attend_tile_rows(int d) { return d == 256 ? 128 : 256; }
+// Waves of a workgroup, and query rows of its tile, where the waves have rows
+// of their own (attend_rows_kernel): 32 rows a wave, 16 at D = 256.
+constexpr int attend_row_waves(int d) { return d == 256 ? 8 : 12; }
+constexpr int attend_tile_rows(int d) { return attend_row_waves(d) * (d == 256 ? 16 : 32); }
 
 // Launchers.  Weak, so that the host half links without the kernels, as the
 // tests of its argument checks build it; a call then reports KVC_E_HIP.
