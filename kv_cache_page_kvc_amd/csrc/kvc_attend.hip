@@ -788,7 +788,8 @@ template <int D>
 hipError_t launch_tile(const AttendParams& p, uint32_t codec, uint32_t rows, hipStream_t stream) {
   constexpr int M = attend_tile_rows(D);
   if (rows == 16) return launch_codec<D, 1, false>(p, codec, stream);
-  if (rows == 32) return launch_codec<D, 2, false>(p, codec, stream);
+  if constexpr (D < 256)
+    if (rows == 32) return launch_codec<D, 2, false>(p, codec, stream);
   if (rows == M) return launch_codec<D, M / (16 * attend_row_waves(D)), true>(p, codec, stream);
   return hipErrorInvalidValue;
 }

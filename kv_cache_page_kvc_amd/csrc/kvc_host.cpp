@@ -804,30 +804,46 @@ struct AttendPlan {
   uint32_t rows = 16, splits = 1, chunk = 0;
   size_t workspace = 0;
 };
-// Context splits, in workgroups of the whole launch.  Few rows (a tile's four
-// waves share the context): at least 512 to fill 256 CUs, shares of 1024
-// positions beyond that to even out ragged lengths, at most 4096 for their
-// join.  Many rows: one workgroup a CU is resident, and every split costs a
-// pass over its rows' partial sums.
+// Two kernels: in attend_kernel a tile of 16 or 32 rows has its workgroup's
+// four waves share the context, in attend_rows_kernel every wave has rows of
+// its own.  The second reads the cache once for 384 rows (128 at D = 256) and
+// is twice as fast at it, but wants long contexts or many workgroups: with
+// fewer than kAttendRowsFew of them and at most kAttendShort positions the
+// first is taken (one 512-row prompt of 32 heads: 15 us against 38; 40 rows of
+// each of 32 sequences with 4000 positions: 130 against 113).  At D = 256 its
+// tiles have 16 rows: 32 spill (49 us against 75 for 16 x 4 drafted rows).
+constexpr uint64_t kAttendRowsFew = 128, kAttendShort = 2048;
+// Context splits, in workgroups of the whole launch.  attend_kernel: at least
+// 512 to fill 256 CUs, shares of 1024 positions beyond that to even out ragged
+// lengths (64 users, 500 to 8000 positions: 123 us; shares of 512: 128, of
+// 2048: 134), at most 4096 for their join.  attend_rows_kernel: one workgroup
+// a CU is resident, and every split costs a pass over its rows' partial sums.
 constexpr uint64_t kAttendFill = 512, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
   const uint64_t most_rows = std::min(b->max_rows, b->n_rows), most = most_rows * G;
-  p->rows = most <= 16 ? 16 : (most <= 64 ? 32 : attend_tile_rows((int)c->head_dim));
-  p->b = batch_view(b, std::max<uint64_t>(1, (most + p->rows - 1) / p->rows), G, p->rows, 1, &p->units);
-  p->join = batch_view(b, std::max<uint64_t>(1, most_rows), 1, 1, 0, &p->join_units);
-  const uint64_t groups = p->units * c->kv_heads;
+  const uint32_t D = c->head_dim, many = (uint32_t)attend_tile_rows((int)D);
+  auto tiles = [&](uint32_t rows) {
+    p->rows = rows;
+    p->b = batch_view(b, std::max<uint64_t>(1, (most + rows - 1) / rows), G, rows, 1, &p->units);
+    return p->units * c->kv_heads;
+  };
   // most positions that one tile's rows see, from a multiple of 64 on
-  uint64_t span = b->max_len;
-  if (o->window && (o->flags & KVC_ATTEND_CAUSAL))
-    span = std::min<uint64_t>(span, (uint64_t)o->window + p->rows / G + 1 + 64);
+  auto seen = [&]() -> uint64_t {
+    if (!o->window || !(o->flags & KVC_ATTEND_CAUSAL)) return b->max_len;
+    return std::min<uint64_t>(b->max_len, (uint64_t)o->window + p->rows / G + 1 + 64);
+  };
+  uint64_t groups = tiles(many);
+  if (most <= 32 || (groups < kAttendRowsFew && seen() <= kAttendShort)) groups = tiles(most <= 16 || D == 256 ? 16 : 32);
+  const uint64_t span = seen();
+  p->join = batch_view(b, std::max<uint64_t>(1, most_rows), 1, 1, 0, &p->join_units);
   uint64_t splits = 1;
-  if (groups && p->rows <= 32)
+  if (groups && p->rows != many)
     splits = std::min((kAttendMost + groups - 1) / groups,
                       std::max((kAttendFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare));
   else if (groups)
-    splits = (kAttendRowsFill + groups - 1) / groups;
+    splits = std::min((kAttendRowsFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare);
   splits = std::min<uint64_t>({splits, (span + kAttendChunk - 1) / kAttendChunk, kMaxSplits});
   splits = std::max<uint64_t>(splits, 1);
   p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
