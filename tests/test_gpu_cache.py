@@ -79,6 +79,11 @@ class World:
         odd = self.host.write(self.table, cu, lengths, k.float().numpy(), v.float().numpy())
         return b, cu, odd
 
+    def widen(self, columns):
+        """A wider block table, so that batches promise longer contexts than there are: other kernels and splits."""
+        more = np.full((self.table.shape[0], max(columns - self.table.shape[1], 0)), 0x7FFFFFFF, np.int64)
+        self.table = np.concatenate([self.table, more], 1)
+
     def fill(self, ctx, lengths):
         self.write(ctx, lengths, lengths)
         self.check_pool("fill")
@@ -111,7 +116,8 @@ class World:
             g = z.double().cpu().numpy()
             assert np.array_equal(g == -np.inf, want_z == -np.inf)
             fin = np.isfinite(want_z)
-            assert (np.abs(g - want_z)[fin] <= off_z[fin]).all(), np.abs(g - want_z)[fin].max()
+            far = np.abs(g[fin] - want_z[fin])
+            assert (far <= off_z[fin]).all(), far.max()
 
 
 # ------------------------------------------------------------------ write
@@ -269,11 +275,28 @@ def test_attend_prompts_and_chunks(ctx, codec, D, T, H, G):
     lengths = [200, 65, 129, 16, 300, 7]
     w = World(codec, H, D, T, lengths, "bf16", seed=6)
     w.fill(ctx, lengths)
-    w.attend(ctx, lengths, lengths, G)                                    # whole prompts
-    w.attend(ctx, [33, 1, 128, 3, 77, 0], lengths, G)                     # chunks behind a past
-    w.attend(ctx, [5, 5, 2, 5, 5, 5], lengths, G, window=20)              # drafts with a window
-    w.attend(ctx, lengths, lengths, G, window=70)
-    w.attend(ctx, [40, 65, 3, 16, 9, 7], lengths, G, causal=False)
+    for columns in (0, 2200 // T):                                        # few rows a tile, then many
+        w.widen(columns)
+        w.attend(ctx, lengths, lengths, G)                                # whole prompts
+        w.attend(ctx, [33, 1, 128, 3, 77, 0], lengths, G)                 # chunks behind a past
+        w.attend(ctx, [5, 5, 2, 5, 5, 5], lengths, G, window=20)          # drafts with a window
+        w.attend(ctx, lengths, lengths, G, window=70)
+        w.attend(ctx, [40, 65, 3, 16, 9, 7], lengths, G, causal=False)
+        w.attend(ctx, [40, 65, 3, 16, 9, 7], lengths, G, causal=False, window=11)
+
+
+@pytest.mark.parametrize("codec,D,H,G,dtype", [("INT8", 128, 2, 4, "fp16"), ("FP8_DYNAMIC", 64, 1, 8, "bf16"),
+                                               ("FP8_DYNAMIC", 256, 1, 3, "fp16"), ("INT8", 32, 3, 5, "bf16")])
+def test_attend_many_rows(ctx, codec, D, H, G, dtype):
+    """Several tiles of many rows, several splits, ragged: ends that fall inside tiles, waves without rows."""
+    print(f"[case] attend many {codec} D={D} H={H} G={G}", flush=True)
+    lengths = [2600, 130, 700, 1, 0]
+    w = World(codec, H, D, 32, lengths, dtype, seed=21)
+    w.fill(ctx, lengths)
+    w.attend(ctx, [300, 130, 257, 1, 0], lengths, G)
+    w.attend(ctx, [97, 64, 40, 1, 0], lengths, G, window=600)
+    w.widen(400)                                           # 12,800 positions promised: a split sees nothing
+    w.attend(ctx, [300, 130, 257, 1, 0], lengths, G)
 
 
 def test_attend_long_context_splits(ctx):
@@ -295,8 +318,9 @@ def test_attend_rows_that_see_nothing(ctx, dtype):
     lengths = [0, 3, 100, 5]
     w = World("INT8", 2, 64, 16, lengths, dtype, seed=11)
     w.fill(ctx, lengths)
-    for rows in ([2, 7, 1, 5], [2, 7, 40, 9], [300, 0, 0, 5]):
+    for rows in ([2, 7, 1, 5], [2, 7, 40, 9], [300, 0, 0, 5], [40, 7, 40, 9]):
         for causal in (True, False):
+            w.widen(200 if rows[0] == 40 else 0)
             out, z, _ = w.attend(ctx, rows, lengths, 3, causal=causal)
             assert bool((out[:2] == 0).all()) and bool((z[:2] == -float("inf")).all())
             if causal and rows[1] == 7:
@@ -319,27 +343,33 @@ def test_attend_ignores_what_was_not_written(ctx):
     w.attend(ctx, [1], [70], 2)
     w.attend(ctx, [70], [70], 2)
     w.attend(ctx, [3], [64], 2)                            # a shorter length hides the third page
+    w.widen(100)
+    w.attend(ctx, [70], [70], 2)
+    w.attend(ctx, [64], [64], 2)
 
 
-def test_attend_query_specials(ctx):
+@pytest.mark.parametrize("columns", [0, 200], ids=["few", "many"])
+def test_attend_query_specials(ctx, columns):
     """A row of zeros, tiny and huge rows, and NaN / infinite rows, which are NaN by themselves."""
     lengths = [50]
     for dtype in ("bf16", "fp16"):
         w = World("INT8", 1, 128, 16, lengths, dtype, seed=13)
         w.fill(ctx, lengths)
-        q = w.values(6, 2)
+        w.widen(columns)
+        q = w.values(6 if not columns else 40, 2)
         q[0] = 0.0
         q[1] = q[1] * 1e-6
         q[1, 0, 5] = torch.finfo(w.dt).smallest_normal / 8
         q[3, 1, 7] = float("nan")
         q[4, 0, 100] = float("inf")
-        b, cu = w.batch([6], lengths)
-        out = torch.zeros((6, 2, 128), dtype=w.dt, device="cuda")
-        z = torch.zeros((6, 2), device="cuda")
+        n = q.shape[0]
+        b, cu = w.batch([n], lengths)
+        out = torch.zeros((n, 2, 128), dtype=w.dt, device="cuda")
+        z = torch.zeros((n, 2), device="cuda")
         o = kvc.Attend(2)
         ws = torch.zeros(kvc.kvc_plan_attend(w.cache, b, o) + 16, dtype=torch.uint8, device="cuda")
         kvc.kvc_cache_attend(ctx, w.cache, b, o, q.cuda(), out, z, ws)
-        bad = torch.zeros(6, 2, dtype=torch.bool)
+        bad = torch.zeros(n, 2, dtype=torch.bool)
         bad[3, 1] = bad[4, 0] = True
         assert torch.equal(out.cpu().isnan(), bad[..., None].expand(-1, -1, 128))
         assert torch.equal(z.cpu().isnan(), bad)
@@ -347,6 +377,60 @@ def test_attend_query_specials(ctx):
         want = ref.attend(w.host, w.table, cu, lengths, clean.float().numpy(), 128 ** -0.5, True, 0)
         keep = ~bad.numpy()
         w.compare(out[~bad.cuda()], z[~bad.cuda()], *(x[keep] for x in want))
+
+
+def test_shared_prefix_and_repeated_pages(ctx):
+    """Two sequences read the same pages, one of them a page twice; each writes its own last page."""
+    w = World("FP8_DYNAMIC", 2, 64, 16, [48, 48], seed=22)
+    w.fill(ctx, [48, 48])
+    w.table[1, :2] = w.table[0, 0]
+    w.attend(ctx, [1, 1], [48, 48], 4)
+    w.attend(ctx, [16, 20], [48, 48], 4)
+    w.write(ctx, [3, 5], [35, 37])
+    w.check_pool()
+    b, cu = w.batch([48, 48], [48, 48])
+    assert kvc.kvc_validate_batch(w.cache, b, w.table, cu, [48, 48], False) == kvc.KVC_OK
+    assert kvc.kvc_validate_batch(w.cache, b, w.table, cu, [48, 48], True) == kvc.KVC_E_DUP_DST
+    k, v = (torch.zeros((96, 2, 64), dtype=w.dt, device="cuda") for _ in range(2))
+    kvc.kvc_cache_read(ctx, w.cache, b, k, v)
+    for got, want in zip((k, v), w.host.read(w.table, cu, [48, 48], 96, w.dt)):
+        assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_offsets_beyond_32_bits(ctx, rows):
+    """Pages 256 MiB apart in pools of 5 GiB, rows 128 MiB apart."""
+    w = World("INT8", 1, 128, 16, [70, 200], "bf16", seed=23)
+    P, gap = w.host.k.shape[0], 1 << 28
+    assert P * gap > 1 << 32
+    pools = [torch.zeros(P * gap, dtype=torch.int8, device="cuda") for _ in range(2)]
+    k, v, ks, vs = w.dev
+    wide_k = pools[0].as_strided((P, 1, 16, 128), (gap, 16 * 128, 128, 1))
+    wide_v = pools[1].as_strided((P, 1, 128, 16), (gap, 16 * 128, 16, 1))
+    wide_k.copy_(k), wide_v.copy_(v)
+    w.dev = (wide_k, wide_v, ks, vs)
+    w.cache = kvc.Cache(*w.dev)
+    w.write(ctx, [70, 200], [70, 200])
+    w.check_pool()
+    w.widen(200)
+    n = 2 * rows
+    far = torch.zeros(n << 26, dtype=torch.bfloat16, device="cuda")
+    q = far.as_strided((n, 2, 128), (1 << 26, 128, 1))
+    x = w.values(n, 2)
+    q.copy_(x)
+    b, cu = w.batch([rows, rows], [70, 200])
+    o = kvc.Attend(2)
+    z = torch.zeros((n, 2), device="cuda")
+    ws = torch.zeros(kvc.kvc_plan_attend(w.cache, b, o) + 16, dtype=torch.uint8, device="cuda")
+    result = far.as_strided((n, 2, 128), (1 << 26, 128, 1), 512)
+    kvc.kvc_cache_attend(ctx, w.cache, b, o, q, result, z, ws)
+    want = ref.attend(w.host, w.table, cu, [70, 200], x.float().numpy(), 128 ** -0.5, True, 0)
+    w.compare(result, z, *want)
+    rk = far.as_strided((n, 1, 128), (1 << 26, 128, 1), 1024)
+    rv = far.as_strided((n, 1, 128), (1 << 26, 128, 1), 2048)
+    kvc.kvc_cache_read(ctx, w.cache, b, rk, rv)
+    for got, exp in zip((rk, rv), w.host.read(w.table, cu, [70, 200], n, torch.bfloat16)):
+        assert torch.equal(got.cpu(), exp)
 
 
 def test_attend_scales_far_apart(ctx):
@@ -383,19 +467,22 @@ def test_bad_metadata_is_reported_and_not_followed(ctx):
         w.table = good.copy()
         w.table[1, 1] = table_bad
         flags = torch.zeros(4, dtype=torch.int32, device="cuda")
-        w.host_table = good
         # attention hides the page's 16 positions from sequence 1
-        b, cu = w.batch([2] * 4, lengths, flags=flags)
-        q = w.values(8, 4)
-        out, z = torch.zeros((8, 4, 64), dtype=w.dt, device="cuda"), torch.zeros((8, 4), device="cuda")
-        o = kvc.Attend(4)
-        ws = torch.zeros(kvc.kvc_plan_attend(w.cache, b, o) + 16, dtype=torch.uint8, device="cuda")
-        kvc.kvc_cache_attend(ctx, w.cache, b, o, q.cuda(), out, z, ws)
-        assert flags.tolist() == [0, 2, 0, 0]
-        for s in range(4):
-            one = ref.attend(w.host, good[s:s + 1], [0, 2], lengths[s:s + 1], q[2 * s:2 * s + 2].float().numpy(), 64 ** -0.5,
-                             True, 0, (1,) if s == 1 else ())
-            w.compare(out[2 * s:2 * s + 2], z[2 * s:2 * s + 2], *one)
+        for n, columns in ((2, 0), (20, 0), (20, 200)):
+            w.widen(columns)
+            flags.zero_()
+            b, cu = w.batch([n] * 4, lengths, flags=flags)
+            q = w.values(4 * n, 4)
+            out, z = torch.zeros((4 * n, 4, 64), dtype=w.dt, device="cuda"), torch.zeros((4 * n, 4), device="cuda")
+            o = kvc.Attend(4)
+            ws = torch.zeros(kvc.kvc_plan_attend(w.cache, b, o) + 16, dtype=torch.uint8, device="cuda")
+            kvc.kvc_cache_attend(ctx, w.cache, b, o, q.cuda(), out, z, ws)
+            assert flags.tolist() == [0, 2, 0, 0]
+            for s in range(4):
+                r = slice(n * s, n * s + n)
+                one = ref.attend(w.host, good[s:s + 1], [0, n], lengths[s:s + 1], q[r].float().numpy(), 64 ** -0.5,
+                                 True, 0, (1,) if s == 1 else ())
+                w.compare(out[r], z[r], *one)
         # reads give zeros there, writes leave everything else alone
         flags.zero_()
         b, cu = w.batch(lengths, lengths, flags=flags)
