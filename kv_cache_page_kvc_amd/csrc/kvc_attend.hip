@@ -5,7 +5,7 @@
 //   w_ij = 2^(t_ij - m_i),  m_i 4 below a running reference of the t_ij
 //   out_i = sum_j w_ij vcode_j / sum_j w_ij / vs[page(j)].
 // Folding log2(vs) into the exponent makes w the weight of a *code*: V's codes
-// then enter the product as they are, and w <= 2^15 is a binary16 value
+// then enter the product as they are, and w < 2^16 is a binary16 value
 // whatever the pages' scales are.  Both products run on the matrix cores in
 // binary16 with binary32 sums: E4M3FN and INT8 codes are binary16 values
 // exactly, a query row is scaled by a power of two to a largest |q| in
@@ -14,15 +14,22 @@
 // themselves at most, and by 2^-29 of the largest where they are below 2^-18
 // of it).  The denominator, the maxima and the merged sums are binary32.
 //
-// Registers instead of LDS.  A wave takes 64 positions at a time as 4 groups
-// of 16 (a group lies in one page).  Scores are computed transposed, S^T =
+// Operands without a transpose.  A wave takes 64 positions at a time as 4
+// groups of 16 (a group lies in one page).  Scores are computed transposed, S^T =
 // K Q^T, with row 4g + j of product tile i standing for position 16g + 4i + j:
 // after 4 tiles lane group g (16 lanes, one query row each) holds the scores
 // of the 16 positions of group g, which is exactly the operand layout of the
-// second product, out^T = V^T W^T, when V is stored token-minor.  So scores,
-// weights and both operands stay in registers, a lane's loads are 16
-// consecutive bytes of K (dimensions) and V (positions), and the running
-// maximum needs two lane swaps a row.
+// second product, out^T = V^T W^T, when V is stored token-minor.  So scores
+// and weights stay in registers, a lane's loads are 16 consecutive bytes of K
+// (dimensions) and of V (positions), and a row's maximum takes two lane swaps.
+//
+// attend_kernel, for single tokens, drafts and short calls, is bound by the
+// cache's bytes: 64 users of 500 to 8000 positions (557 MB) take 123 us, 4.5
+// TB/s, where a copy reaches 5.0.  attend_rows_kernel, for prompts, is bound
+// by the vector instructions around the matrix instructions -- an exponential,
+// a fused multiply-add, a sum, half a conversion and a maximum a score, of 64
+// scores a lane and tile -- at 1.0 PFLOP/s on an 8192-row prompt, where a large
+// binary16 product of the library reaches 1.4.
 #include <type_traits>
 
 #include "kvc_cache_device.h"
@@ -93,7 +100,8 @@ __device__ __forceinline__ void lds_barrier() {
 struct Tile {
   Seq s;
   int rows, row0;        // rows of the sequence (token * group + head), first of the tile
-  int begin, end;        // positions that some row of the tile sees; begin is a multiple of kTile
+  int from, end;         // positions that some row of the tile sees
+  int begin;             // `from`, down to a multiple of kTile
   int all_from, all_to;  // positions that every row of the tile sees
 };
 // the tile of m rows that starts at row0
@@ -107,7 +115,8 @@ __device__ __forceinline__ bool make_tile(const AttendParams& p, const Seq& s, i
   const int first = t.row0 / (int)p.group, last = min(t.rows - 1, t.row0 + m - 1) / (int)p.group;
   t.end = p.causal ? max(0, min(t.s.len, t.s.start + last + 1)) : t.s.len;
   t.all_to = p.causal ? min(t.s.len, t.s.start + first + 1) : t.s.len;
-  t.begin = (p.window ? max(0, t.s.start + first - (int)p.window + 1) : 0) / kTile * kTile;
+  t.from = p.window ? max(0, t.s.start + first - (int)p.window + 1) : 0;
+  t.begin = t.from / kTile * kTile;
   t.all_from = p.window ? t.s.start + last - (int)p.window + 1 : 0;
   return true;
 }
@@ -271,7 +280,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
     int32_t pv = next_v, pk = next_k;
     page_ids(tile + kWaves, next_v, next_k);                // used one tile later
     const bool okv = pv >= 0 && (uint32_t)pv < p.c.num_pages, okk = pk >= 0 && (uint32_t)pk < p.c.num_pages;
-    bad_page = bad_page || !okv;
+    bad_page |= !okv & (base + 16 * g + 15 >= t.from) & (base + 16 * g < t.end);   // where a row looks
     pv = okv ? pv : 0;
     pk = okk ? pk : 0;
     const int gv = (16 * min(4 * tile + g, last_group)) & (T - 1);
@@ -416,11 +425,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 }
 
 // Many rows: every wave of the workgroup has 16 * NT rows of its own, and the
-// context's tiles go through LDS, converted to binary16 once for all of them.  LDS holds operand fragments in the order the lanes read them (64
-// lanes x 16 bytes each), so neither side has bank conflicts; while a tile is
-// worked on, the codes of the next one are on their way into registers, and
-// they are converted into the other half of the buffer.  Waves 0 .. 3 stage
-// the tile's K, each one product tile of 16 positions, waves 4 .. 7 its V.
+// context's tiles go through LDS, converted to binary16 once for all of them.
+// LDS holds operand fragments in the order the lanes read them (64 lanes x 16
+// bytes each), so neither side has bank conflicts; while tiles are worked on,
+// the codes of a later one are on their way into registers, and they are
+// converted into the other half of the ring.  Waves 0 .. 3 stage a tile's K,
+// each one product tile of 16 positions, waves 4 .. 7 its V.
 // Twelve waves, three a SIMD, hide each other's latencies best: an 8192-row
 // prompt of 32 heads took 522 us, with eight waves and fragments read a phase
 // ahead 529 (and 519 against 556 for chunks of INT8); at D = 256 the output's
@@ -499,7 +509,8 @@ __global__ __launch_bounds__(64 * attend_row_waves(D), attend_row_waves(D) / 4) 
       }
     }
     if (of_v) {
-      bad_page = bad_page || !ok;
+      const int at_group = tile * kTile + 16 * g;
+      bad_page |= !ok & (at_group + 15 >= t.from) & (at_group < t.end);      // where a row looks
       valid_in = ok ? min(max(t.s.len - tile * kTile - 16 * g, 0), 16) : 0;
       if (part == 0) {
         const uint64_t i = (uint64_t)page * p.c.stride_scale + h;
@@ -653,7 +664,8 @@ __global__ __launch_bounds__(64 * attend_row_waves(D), attend_row_waves(D) / 4) 
 
 // Joins the context splits of one row and query head, one workgroup of WAVES
 // each: the lanes take the splits' maxima and sums, then each wave adds up its
-// share of the splits' partial sums, eight loads in flight.
+// share of the splits' partial sums, eight loads in flight (3 rows x 4 heads of
+// 256 splits: 7.5 us with sixteen waves; four took 11.5 for 512).
 template <int D, int M, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attend_join_kernel(AttendParams p, BatchView rows) {
   constexpr int E = D >= 64 ? D / 64 : 1;                 // dimensions of a lane

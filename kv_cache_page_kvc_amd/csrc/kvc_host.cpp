@@ -665,6 +665,7 @@ hipError_t run_decode(const CallParams& P, const kvc_layout* L, const Plan& plan
 // ------------------------------------------------------------------ resident 8-bit cache
 // every index the kernels form from these fits 32 bits
 constexpr uint64_t kMaxSeqs = 1u << 20, kMaxRows = 1u << 30, kMaxLen = 1u << 30;
+constexpr uint64_t kMaxThreads = 0xFFFFFFFFull;   // of a launch
 
 kvc_status check_cache(const kvc_cache* c) {
   if (!c || c->abi != KVC_ABI_VERSION || c->reserved) return KVC_E_ARG;
@@ -786,7 +787,7 @@ kvc_status rows_call(kvc_ctx* ctx, const kvc_cache* c, const kvc_batch* b, const
   P.k = rows_view(k);
   P.v = rows_view(v);
   P.units = (uint32_t)units;
-  if (units * c->kv_heads * 2 * (T / 16) >= 0x7FFFFFFFull) return KVC_E_ARG;
+  if (units * c->kv_heads * 2 * (T / 16) * 64 + 512 > kMaxThreads) return KVC_E_ARG;
   if (!(write ? launch_cache_write : launch_cache_read)) return KVC_E_HIP;
   DeviceGuard g(ctx->device);
   if (!g.ok) return KVC_E_HIP;
@@ -848,7 +849,9 @@ kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend*
   splits = std::max<uint64_t>(splits, 1);
   p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
   p->splits = (uint32_t)std::max<uint64_t>(1, (span + p->chunk - 1) / p->chunk);
-  if (groups * p->splits > 0x7FFFFFFFull || p->join_units * o->q_heads > 0x7FFFFFFFull) return KVC_E_ARG;
+  const uint64_t threads = p->rows == many ? 64 * attend_row_waves((int)D) : 256;
+  if (groups * p->splits * threads > kMaxThreads) return KVC_E_ARG;
+  if (p->splits > 1 && p->join_units * o->q_heads * 1024 > kMaxThreads) return KVC_E_ARG;
   p->workspace = p->splits == 1 ? 0 : (size_t)p->splits * b->n_rows * o->q_heads * (c->head_dim + 2) * sizeof(float);
   return KVC_OK;
 }

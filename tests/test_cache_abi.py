@@ -22,8 +22,8 @@ def cache(H=4, D=128, T=16, P=64, **more):
     return c
 
 
-def batch(n=3, n_rows=10, max_rows=6, max_len=100, columns=8, **more):
-    b = kvc.kvc_batch(n, n_rows, max_rows, max_len, columns, FAKE + (1 << 35), FAKE + (1 << 36), FAKE + (1 << 37), None)
+def batch(n_seqs=3, n_rows=10, max_rows=6, max_len=100, columns=8, **more):
+    b = kvc.kvc_batch(n_seqs, n_rows, max_rows, max_len, columns, FAKE + (1 << 35), FAKE + (1 << 36), FAKE + (1 << 37), None)
     for k, v in more.items():
         setattr(b, k, v)
     return b
@@ -94,6 +94,14 @@ def test_rows_calls_refuse_bad_arguments(fn):
     assert write(b=batch(n_rows=0), k=rows(data=None), v=rows(data=None), ctx=CTX, fn=fn) == kvc.KVC_OK
 
 
+def test_launches_that_are_too_large_are_refused():
+    huge = dict(n_seqs=1, n_rows=1 << 30, max_rows=1 << 30, max_len=1 << 30, stride_table=1 << 26)
+    for fn in ("kvc_cache_write", "kvc_cache_read"):
+        assert write(b=batch(**huge), fn=fn, ctx=CTX) == kvc.KVC_E_ARG
+    assert attend(b=batch(n_seqs=1 << 20, n_rows=1 << 29, max_rows=1 << 20, max_len=1 << 12, stride_table=1 << 8),
+                  q=rows(4), out=rows(4), o=options(q_heads=4), ctx=CTX) == kvc.KVC_E_ARG
+
+
 def test_outputs_must_not_overlap():
     half = dict(stride_row=2 * 128)                        # rows of 4 heads x 128 at half their size
     assert write(k=rows(**half), fn="kvc_cache_read") == kvc.KVC_E_ARG
@@ -130,7 +138,7 @@ def test_attend_workspace():
     c, o = cache(P=1 << 20), options()
     # short contexts are not split
     assert L.kvc_plan_attend(R(c), R(batch()), R(o), ctypes.byref(n)) == kvc.KVC_OK and n.value == 0
-    long = batch(n=2, n_rows=2, max_rows=1, max_len=100000, columns=8192)
+    long = batch(n_seqs=2, n_rows=2, max_rows=1, max_len=100000, columns=8192)
     assert L.kvc_plan_attend(R(c), R(long), R(o), ctypes.byref(n)) == kvc.KVC_OK
     per_split = 2 * 8 * (128 + 2) * 4
     assert n.value > per_split and n.value % per_split == 0

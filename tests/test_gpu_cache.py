@@ -333,6 +333,46 @@ def test_attend_rows_that_see_nothing(ctx, dtype):
     assert bool((out[4:] == 7.0).all()) and bool((z[4:] == 7.0).all()) and not bool((out[1:4] == 7.0).any())
 
 
+def test_pages_before_the_window_may_be_gone(ctx):
+    """Table entries that no row looks at any more are neither followed nor reported."""
+    w = World("INT8", 1, 64, 16, [300, 90], seed=24)
+    w.fill(ctx, [300, 90])
+    real = w.table.copy()
+    for rows, columns in (([1, 1], 0), ([20, 33], 200)):
+        w.table = real.copy()
+        w.widen(columns)
+        flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+        for b in range(2):
+            first = [300, 90][b] - rows[b] - 30 + 1        # the first position that a row sees
+            w.table[b, :first // 16] = -1
+        gone = w.table
+        b, cu = w.batch(rows, [300, 90], flags=flags)
+        q = w.values(sum(rows), 2)
+        out, z = torch.zeros((sum(rows), 2, 64), dtype=w.dt, device="cuda"), torch.zeros((sum(rows), 2), device="cuda")
+        o = kvc.Attend(2, window=30)
+        ws = torch.zeros(kvc.kvc_plan_attend(w.cache, b, o) + 16, dtype=torch.uint8, device="cuda")
+        kvc.kvc_cache_attend(ctx, w.cache, b, o, q.cuda(), out, z, ws)
+        assert flags.tolist() == [0, 0] and gone[0, 0] == -1
+        w.compare(out, z, *ref.attend(w.host, real, cu, [300, 90], q.float().numpy(), 64 ** -0.5, True, 30))
+
+
+def test_nothing_cached(ctx):
+    """max_len 0 and a block table without columns: rows come back empty, writes store nothing."""
+    w = World("FP8_DYNAMIC", 2, 32, 16, [0, 0], "fp16", seed=25)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = kvc.Batch(torch.zeros((2, 0), **i32), torch.tensor([0, 3, 5], **i32), torch.zeros(2, **i32), 5, 3, 0)
+    k, v = (torch.full((5, 2, 32), 7.0, dtype=w.dt, device="cuda") for _ in range(2))
+    kvc.kvc_cache_write(ctx, w.cache, b, k, v)
+    w.check_pool()
+    kvc.kvc_cache_read(ctx, w.cache, b, k, v)
+    assert not bool(k.any()) and not bool(v.any())
+    for heads in (2, 64):
+        q = w.values(5, heads)
+        out, z = torch.full((5, heads, 32), 7.0, dtype=w.dt, device="cuda"), torch.zeros((5, heads), device="cuda")
+        kvc.kvc_cache_attend(ctx, w.cache, b, kvc.Attend(heads), q.cuda(), out, z)
+        assert not bool(out.any()) and bool((z == -float("inf")).all())
+
+
 def test_attend_ignores_what_was_not_written(ctx):
     """The last page's unwritten tokens hold NaN codes, and pages behind the sequence NaN scales."""
     w = World("FP8_DYNAMIC", 1, 64, 32, [70], seed=12)
