@@ -431,12 +431,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 // the codes of a later one are on their way into registers, and they are
 // converted into the other half of the ring.  Waves 0 .. 3 stage a tile's K,
 // each one product tile of 16 positions, waves 4 .. 7 its V.
-// Twelve waves, three a SIMD, hide each other's latencies best: an 8192-row
-// prompt of 32 heads took 522 us, with eight waves and fragments read a phase
-// ahead 529 (and 519 against 556 for chunks of INT8); at D = 256 the output's
-// registers allow eight.
+// At D = 128 twelve waves, three a SIMD, hide each other's latencies best: an
+// 8192-row prompt of 32 heads takes 528 us, with eight waves and fragments read
+// a phase ahead 529 (chunks of INT8 520 against 556).  Eight waves of 48 rows,
+// which read a third less from LDS, take 600 and 602, products of 32 x 32
+// scores with half the matrix instructions 577 and 597: neither LDS nor the
+// matrix units are what it waits for.
 template <int D, int NT, uint32_t CODEC>
-__global__ __launch_bounds__(64 * attend_row_waves(D), attend_row_waves(D) / 4) void attend_rows_kernel(AttendParams p) {
+__global__ __launch_bounds__(64 * attend_row_waves(D), attend_row_waves(D) * attend_row_resident(D) / 4)
+void attend_rows_kernel(AttendParams p) {
   constexpr int M = 16 * NT * attend_row_waves(D), KS = D / 32, NV = D / 16, CH = D >= 64 ? D / 64 : 1;
   constexpr int V0 = 4 * KS;           // V's fragments come behind K's
   // A ring of tiles: half of them are worked on between two barriers while

@@ -55,9 +55,15 @@ struct AttendParams {
   uint32_t join_units;
 };
 constexpr uint32_t kMaxSplits = 2048;
-// Waves of a workgroup, and query rows of its tile, where the waves have rows
-// of their own (attend_rows_kernel): 32 rows a wave, 16 at D = 256.
-constexpr int attend_row_waves(int d) { return d == 256 ? 8 : 12; }
+// attend_rows_kernel: waves of a workgroup, workgroups that a CU holds (by LDS
+// and registers), query rows of a workgroup (32 a wave, 16 at D = 256).  At
+// D <= 64 two workgroups of eight waves work while the other one waits at its
+// barrier: two 4096-row prompts of 32 heads of 64 take 209 us, 512-row chunks
+// over 16,000 positions 310; with one workgroup of twelve it was 219 and 512,
+// with one of sixteen 195 and 331, but 171 against 144 for 16 x 1024 rows.
+// D = 256: twelve waves are no faster (101 us against 103, 52 against 46 for 64 rows).
+constexpr int attend_row_waves(int d) { return d == 128 ? 12 : 8; }
+constexpr int attend_row_resident(int d) { return d <= 64 ? 2 : 1; }
 constexpr int attend_tile_rows(int d) { return attend_row_waves(d) * (d == 256 ? 16 : 32); }
 
 // Launchers.  Weak, so that the host half links without the kernels, as the

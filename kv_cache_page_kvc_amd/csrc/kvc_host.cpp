@@ -807,8 +807,8 @@ struct AttendPlan {
 };
 // Two kernels: in attend_kernel a tile of 16 or 32 rows has its workgroup's
 // four waves share the context, in attend_rows_kernel every wave has rows of
-// its own.  The second reads the cache once for 384 rows (128 at D = 256) and
-// is twice as fast at it, but wants long contexts or many workgroups: with
+// its own.  The second reads the cache once for 128 to 384 rows and is twice
+// as fast at it, but wants long contexts or many workgroups: with
 // fewer than kAttendRowsFew of them and at most kAttendShort positions the
 // first is taken (one 512-row prompt of 32 heads: 15 us against 38; 40 rows of
 // each of 32 sequences with 4000 positions: 130 against 113).  At D = 256 its
@@ -817,8 +817,8 @@ constexpr uint64_t kAttendRowsFew = 128, kAttendShort = 2048;
 // Context splits, in workgroups of the whole launch.  attend_kernel: at least
 // 512 to fill 256 CUs, shares of 1024 positions beyond that to even out ragged
 // lengths (64 users, 500 to 8000 positions: 123 us; shares of 512: 128, of
-// 2048: 134), at most 4096 for their join.  attend_rows_kernel: one workgroup
-// a CU is resident, and every split costs a pass over its rows' partial sums.
+// 2048: 134), at most 4096 for their join.  attend_rows_kernel: as many as
+// are resident; every split costs a pass over its rows' partial sums.
 constexpr uint64_t kAttendFill = 512, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
@@ -844,7 +844,8 @@ kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend*
     splits = std::min((kAttendMost + groups - 1) / groups,
                       std::max((kAttendFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare));
   else if (groups)
-    splits = std::min((kAttendRowsFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare);
+    splits = std::min((kAttendRowsFill * attend_row_resident((int)D) + groups - 1) / groups,
+                      (span + kAttendShare - 1) / kAttendShare);
   splits = std::min<uint64_t>({splits, (span + kAttendChunk - 1) / kAttendChunk, kMaxSplits});
   splits = std::max<uint64_t>(splits, 1);
   p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
