@@ -51,6 +51,7 @@ struct AttendParams {
   float scale_log2;                         // softmax scale * log2(e)
   uint32_t units;                           // row tiles
   uint32_t splits, chunk;                   // context splits of `chunk` tokens each
+  uint32_t turn_at, turn;                   // attend_rows_kernel's order of tiles: [at, 2 at) turned by so many
   BatchView join;                           // splits > 1: units are rows
   uint32_t join_units;
 };

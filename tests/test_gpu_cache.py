@@ -299,6 +299,14 @@ def test_attend_many_rows(ctx, codec, D, H, G, dtype):
     w.attend(ctx, [300, 130, 257, 1, 0], lengths, G)
 
 
+@pytest.mark.parametrize("rows,length", [(380, 380), (400, 400), (480, 700), (720, 720)])
+def test_attend_one_prompt_of_some_rounds(ctx, rows, length):
+    """One sequence of 8 to 15 tiles a head: with 64 heads 2 to 4 rounds of workgroups, whose order is not the tiles'."""
+    w = World("FP8_DYNAMIC", 64, 128, 16, [length], "bf16", seed=31)
+    w.fill(ctx, [length])
+    w.attend(ctx, [rows], [length], 8)
+
+
 def test_attend_long_context_splits(ctx):
     """One sequence of 40,000 positions among short ones, split and joined."""
     for codec, lengths, G in (("INT8", [40000], 4), ("FP8_DYNAMIC", [9000, 3, 4097, 1], 8)):
