@@ -432,10 +432,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attend_kernel(AttendParams p) 
 // converted into the other half of the ring.  Waves 0 .. 3 stage a tile's K,
 // each one product tile of 16 positions, waves 4 .. 7 its V.
 // At D = 128 twelve waves, three a SIMD, hide each other's latencies best: an
-// 8192-row prompt of 32 heads takes 502 us (530 in its tiles' own order, and then with eight
-// waves and fragments read
-// a phase ahead 529 (chunks of INT8 520 against 556).  Eight waves of 48 rows,
-// which read a third less from LDS, take 600 and 602, products of 32 x 32
+// 8192-row prompt of 32 heads took 522 us, with eight waves and fragments read
+// a phase ahead 529 (chunks of INT8: 519 against 556).  Eight waves of 48 rows,
+// which read a third less from LDS, took 600 and 602, products of 32 x 32
 // scores with half the matrix instructions 577 and 597: neither LDS nor the
 // matrix units are what it waits for.
 template <int D, int NT, uint32_t CODEC>
