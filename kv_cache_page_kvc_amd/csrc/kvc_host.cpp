@@ -817,9 +817,16 @@ constexpr uint64_t kAttendRowsFew = 128, kAttendShort = 2048;
 // Context splits, in workgroups of the whole launch.  attend_kernel: at least
 // 512 to fill 256 CUs, shares of 1024 positions beyond that to even out ragged
 // lengths (64 users, 500 to 8000 positions: 123 us; shares of 512: 128, of
-// 2048: 134), at most 4096 for their join.  attend_rows_kernel: as many as
-// are resident; every split costs a pass over its rows' partial sums.
-constexpr uint64_t kAttendFill = 512, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256;
+// 2048: 134), at most 4096 for their join.  attend_rows_kernel: the last
+// workgroup ends a share of the span after the mean, and every split costs a
+// pass over all rows' partial sums, for a tile's rows about as much as 5 of
+// its positions: the sum is least for sqrt(span * tile / (5 rows)) splits
+// (512 rows a sequence behind 30,000 positions 329 us, 371 where splits only
+// fill the device; 16 x 128 rows behind 4000 to 32,000 853, 1079, and 1309,
+// 1217 if all have 32,000; 2500 rows, no past, 118, 171).  Beyond 16
+// the join is another, dearer for many rows, and pays only for fewer
+// workgroups than the device holds.
+constexpr uint64_t kAttendFill = 512, kAttendShare = 1024, kAttendMost = 4096, kAttendRowsFill = 256, kAttendRowsCost = 5;
 constexpr uint64_t kAttendChunk = 256;       // positions the four waves of one take together
 kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend* o, AttendPlan* p) {
   const uint32_t G = o->q_heads / c->kv_heads;
@@ -843,9 +850,12 @@ kvc_status plan_attend(const kvc_cache* c, const kvc_batch* b, const kvc_attend*
   if (groups && p->rows != many)
     splits = std::min((kAttendMost + groups - 1) / groups,
                       std::max((kAttendFill + groups - 1) / groups, (span + kAttendShare - 1) / kAttendShare));
-  else if (groups)
-    splits = std::min((kAttendRowsFill * attend_row_resident((int)D) + groups - 1) / groups,
-                      (span + kAttendShare - 1) / kAttendShare);
+  else if (groups) {
+    const uint64_t fill = kAttendRowsFill * attend_row_resident((int)D);
+    const uint64_t square = span * many / std::max<uint64_t>(1, kAttendRowsCost * b->n_rows * o->q_heads);
+    while ((splits + 1) * (splits + 1) <= square && (splits < 16 || (splits + 1) * groups <= fill)) splits++;
+    splits = std::min(splits, (span + kAttendShare - 1) / kAttendShare);
+  }
   splits = std::min<uint64_t>({splits, (span + kAttendChunk - 1) / kAttendChunk, kMaxSplits});
   splits = std::max<uint64_t>(splits, 1);
   p->chunk = (uint32_t)std::max<uint64_t>(kAttendChunk, align_up((span + splits - 1) / splits, kAttendChunk));
