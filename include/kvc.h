@@ -492,7 +492,8 @@ kvc_status kvc_cache_attend(kvc_ctx *ctx, const kvc_cache *cache, const kvc_batc
 /* Check host copies of a batch's arrays (block_table [n_seqs][stride_table],
  * cu_rows [n_seqs + 1], lengths [n_seqs]) against its bounds and the cache:
  * KVC_E_ARG for rows or lengths out of bounds, KVC_E_PAGE_RANGE for a page id
- * outside [0, num_pages) below a sequence's length, KVC_E_DUP_DST when
+ * outside [0, num_pages) below a sequence's length (pages that a window has
+ * left behind, which attention does not look at, count too), KVC_E_DUP_DST when
  * `writes` is not 0 and two sequences (or one, twice) would write a page.
  * Host only. */
 kvc_status kvc_validate_batch(const kvc_cache *cache, const kvc_batch *batch, const int32_t *block_table,

@@ -4,6 +4,12 @@ Every step of encode/decode runs in the HIP kernels of ``libkvc.so``; this
 module converts Python/torch arguments into the C structures and calls the
 entry points of the same names.  There is no fallback: if the library is
 missing, importing the binding's functions raises.
+
+Besides the page codecs there is a cache that stays in 8 bits on the GPU:
+``Cache`` describes its pages, ``Batch`` a call's sequences, ``Rows`` a tensor
+of rows [row][head][dim]; ``kvc_cache_write`` quantises new K and V rows into
+it, ``kvc_cache_read`` brings rows back to 16 bits, and ``kvc_cache_attend``
+(options ``Attend``, sizes from ``kvc_plan_attend``) attends over it.
 """
 from __future__ import annotations
 

@@ -28,8 +28,9 @@
 // TB/s, where a copy reaches 5.0.  attend_rows_kernel, for prompts, is bound
 // by the vector instructions around the matrix instructions -- an exponential,
 // a fused multiply-add, a sum, half a conversion and a maximum a score, of 64
-// scores a lane and tile -- at 1.0 PFLOP/s on an 8192-row prompt, where a large
-// binary16 product of the library reaches 1.4.
+// scores a lane and tile -- and by the waits between them, at 1.1 PFLOP/s on an
+// 8192-row prompt (500 us; matrix units 51% busy, vector units 63%), where a
+// large binary16 product of the library reaches 1.4.
 #include <type_traits>
 
 #include "kvc_cache_device.h"

@@ -107,7 +107,13 @@ __device__ __forceinline__ void pair_max(uint32_t w, uint32_t& am, uint32_t& odd
   odd |= fa && fb ? 0u : 1u;
 }
 
-// Waves of an item (page, head, component), and its groups of 16 tokens a wave
+// Waves of an item (page, head, component), and its groups of 16 tokens a wave.
+// A row is read once and stays in registers between its maximum and its codes,
+// so a write moves what it must: 64K tokens of 8 heads of 128 (403 MB in and
+// out) take 82 us, 4.9 TB/s, where a copy reaches 5.0; with the rows read twice
+// it was 124.  Small calls are bound by the chain cu_rows -> block table -> rows
+// -> scale: one token 4.8 us, 256 users' tokens 8.5.  At D = 64 a token's head
+// is 128 bytes, and 24 ragged prompts (116 MB) reach 3.0 TB/s, 38.6 us.
 constexpr int item_waves(int T) { return T >= 128 ? 8 : T / 16; }
 
 template <int D, uint32_t CODEC, int DT, int T>
@@ -267,7 +273,8 @@ __global__ __launch_bounds__(item_waves(T) == 8 ? 512 : 256) void cache_write_ke
   else store(std::true_type{});
 }
 
-// A wave reads 16 tokens of one (page, head, component).
+// A wave reads 16 tokens of one (page, head, component): 64K tokens of 8 heads
+// of 128 take 88 us, 4.6 TB/s, bound by HBM.
 template <int D, uint32_t CODEC, int DT, int T>
 __global__ __launch_bounds__(256) void cache_read_kernel(RowsParams p) {
   constexpr int GROUPS = T / 16;

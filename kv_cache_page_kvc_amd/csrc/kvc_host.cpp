@@ -1,6 +1,7 @@
 // kvc_host.cpp -- host half of libkvc: argument validation, the slot plan,
 // the retained device arena, format constants (Lloyd-Max codebook, sign
-// generator) and the launches.
+// generator), the launches, and the checks and launch shapes of the resident
+// 8-bit cache's calls.
 //
 // Behaviour follows OrbitKV docs, "KV precision and storage encoding":
 //  "FP8 and TurboQuant": layouts and K/V roles are validated explicitly;
