@@ -299,6 +299,17 @@ def test_attend_many_rows(ctx, codec, D, H, G, dtype):
     w.attend(ctx, [300, 130, 257, 1, 0], lengths, G)
 
 
+@pytest.mark.parametrize("codec,D,H,G,rows", [("INT8", 128, 1, 8, 60), ("FP8_DYNAMIC", 64, 2, 4, 90),
+                                              ("INT8", 256, 4, 5, 100)])
+def test_attend_many_rows_many_splits(ctx, codec, D, H, G, rows):
+    """Many rows behind a long context: up to 20 splits, some of which the shorter sequence does not have."""
+    lengths = [20000, 2500]
+    w = World(codec, H, D, 64, lengths, "bf16", seed=41)
+    w.fill(ctx, lengths)
+    w.attend(ctx, [rows, 33], lengths, G)
+    w.attend(ctx, [rows, 33], lengths, G, window=3000)
+
+
 @pytest.mark.parametrize("rows,length", [(380, 380), (400, 400), (480, 700), (720, 720)])
 def test_attend_one_prompt_of_some_rounds(ctx, rows, length):
     """One sequence of 8 to 15 tiles a head: with 64 heads 2 to 4 rounds of workgroups, whose order is not the tiles'."""
